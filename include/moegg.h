@@ -552,6 +552,193 @@ moegg_status_t moegg_grouped_gemm_k_grouped_e8m0(
     const int32_t* t_sizes, int G, int64_t T, int Mw, int Nw, int64_t scale_groups,
     void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The layer around the grouped GEMMs: routing, token permutation, and 8-bit
+ * activation checkpoints.  The conventions at the top hold for these calls
+ * too; none of them but moegg_route takes a workspace, and none sets flags:
+ * what a bad index or count does is said at each call.
+ *
+ * row_of, int32 [T, k], ties them together: row_of[t, j] is the row of A, H, Y
+ * (and of their gradients) that belongs to the j-th expert of token t, or
+ * negative where there is none.  For the masked layout rows are counted
+ * through [G, cap]: row e * cap + r is row r of expert e, and rows_total is
+ * G * cap.  A row_of value outside [0, rows_total) is read as "none".  Each row
+ * belongs to at most one (t, j).
+ */
+
+/* Scores of the router's logits. */
+typedef enum {
+    MOEGG_SCORE_SOFTMAX = 0,     /* softmax over the token's experts */
+    MOEGG_SCORE_SIGMOID = 1      /* 1 / (1 + e^-x), each expert by itself */
+} moegg_score_t;
+
+/* Workspace bytes of moegg_route for T tokens and E experts.  Pure host
+ * function.  Returns 0 for invalid arguments. */
+size_t moegg_route_workspace_bytes(int T, int E);
+
+/*
+ * Routing: logits -> the k experts of every token, their weights, the counts
+ * that the schedule reads, and row_of.
+ *   logits   fp32 (logits_dtype MOEGG_LOGITS_FP32) or bf16 [T, E].  NaN and
+ *            -inf: the expert cannot be chosen.  +inf is read as the largest
+ *            finite number.
+ *   bias     fp32 [E] or NULL: added to the scores for the choice, not for the
+ *            weights (load balancing without an auxiliary loss).  NaN or -inf:
+ *            the expert cannot be chosen.
+ *   ids      int32 [T, k], written: with s the scores and key = s + bias (or
+ *            the logits without a bias), the k experts of the largest keys,
+ *            largest first, ties to the lower id; -1 where fewer than k can be
+ *            chosen.
+ *   n_groups, topk_groups, group_top: experts in n_groups groups of E /
+ *            n_groups consecutive ids; only the topk_groups groups with the
+ *            largest sums of their group_top (1 or 2) largest scores (keys, with
+ *            a bias) take part, ties to the lower group.  n_groups = 1: all.
+ *   weights  fp32 [T, k], written: scale * s[id], divided by the token's sum of
+ *            chosen scores when renorm is not 0; 0 where ids is -1.
+ *   m_sizes  int32 [E], written: assignments of every expert.  With cap they
+ *            are not clamped (the masked call clamps and flags them).
+ *   row_of   int32 [T, k], written: seg_off[e] + r for the contiguous layout
+ *            (cap = 0; seg_off[e] = sum_{j<e} align_up(m_j, seg_align)) or
+ *            e * cap + r for the masked one, where r is the number of earlier
+ *            tokens with expert e; -1 where ids is -1, where r >= cap, and for
+ *            rows at or past rows_total.
+ * Keys with a bias, and sums of two scores, are compared in 64 bits.
+ * Deterministic.  One launch up to 64 tokens, else two.
+ * T = 0..16773120, E = 1..1024, k = 1..32 (and k <= E): UNSUPPORTED beyond
+ * the upper ends.  n_groups divides E, at most 64; 1 <= topk_groups <=
+ * n_groups; group_top 1 or 2; scale > 0 and finite; seg_align >= 1; cap >= 0;
+ * logits and outputs aligned to their elements.  ws: moegg_route_workspace_bytes(T, E), 256-byte aligned.
+ */
+typedef enum { MOEGG_LOGITS_FP32 = 0, MOEGG_LOGITS_BF16 = 1 } moegg_logits_t;
+
+moegg_status_t moegg_route(const void* logits, moegg_logits_t logits_dtype, const float* bias, int32_t* ids,
+                           float* weights, int32_t* m_sizes, int32_t* row_of, int T, int E, int k,
+                           moegg_score_t score, int n_groups, int topk_groups, int group_top, int renorm, float scale,
+                           int64_t rows_total, int seg_align, int cap, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradient of the logits from that of the weights.  The choice has no
+ * gradient, nor has the bias.  ids as moegg_route wrote them (an id outside
+ * [0, E) is none), d_weights fp32 [T, k], d_logits [T, E] of the logits' type,
+ * every element written.  score, renorm and scale as in the forward call.
+ */
+moegg_status_t moegg_route_backward(const void* logits, moegg_logits_t logits_dtype, const int32_t* ids,
+                                    const float* d_weights, void* d_logits, int T, int E, int k, moegg_score_t score,
+                                    int renorm, float scale, void* stream);
+
+/*
+ * Tokens into expert rows: A[row_of[t, j]] = x[t] for every assignment, in the
+ * operand format of the grouped GEMM's dtype.
+ *   x        bf16 [T, K].
+ *   A        MOEGG_BF16: bf16 [rows_total, K].  MOEGG_FP8_E4M3,
+ *            MOEGG_FP8_E4M3_SCALE_KM and MOEGG_FP8_E4M3_E8M0 (also the format
+ *            of MOEGG_FP8_E4M3_FP4_E2M1): e4m3 codes, with A_scale as that call
+ *            takes it: per 1x128 group
+ *                s = amax / 448 (1 if that is 0), codes e4m3_rne(x / s);
+ *            E8M0: s rounded up to a power of two, at least 2^-126.
+ *            A NaN is the code NaN and does not count for the amax; in a group
+ *            with an infinity s is infinite (E8M0: 255) and the codes 0 or NaN.
+ * Rows that no token has keep their contents.  A token is read once, whatever k.
+ * bf16: any K >= 1, pointers 2-byte aligned.  e4m3: K % 128 == 0, x and A
+ * 16-byte aligned, A_scale 4-byte aligned.  k = 1..32.
+ */
+moegg_status_t moegg_dispatch(const void* x, const int32_t* row_of, void* A, void* A_scale, int T, int k, int K,
+                              int64_t rows_total, moegg_dtype_t dtype, void* stream);
+
+/*
+ * Expert rows back into tokens: out[t] = bf16_rne(sum_j weights[t, j] *
+ * Y[row_of[t, j]]) with the sum in fp32 in the order of j; weights NULL: all 1.
+ * A token with no row gets 0.  With weights NULL it is also dispatch's backward
+ * pass (the gradient of x from that of A's rows).
+ *   Y bf16 [rows_total, N], out bf16 [T, N]; any N >= 1, 2-byte aligned; k = 1..32.
+ */
+moegg_status_t moegg_combine(const void* Y, const int32_t* row_of, const float* weights, void* out, int T, int k,
+                             int N, int64_t rows_total, void* stream);
+
+/*
+ * Gradients of moegg_combine: dY[row_of[t, j]] = weights[t, j] * dout[t], in
+ * the operand format of `dtype` as for moegg_dispatch (the products in fp32),
+ * and d_weights[t, j] = sum_n Y[row_of[t, j], n] * dout[t, n] in fp32 (0 where
+ * there is no row).  dY's other rows keep their contents.
+ *   dout bf16 [T, N]; Y bf16 [rows_total, N]; weights, d_weights fp32 [T, k].
+ * MOEGG_BF16: any N, 2-byte aligned.  e4m3: N % 128 == 0, dout, Y and dY
+ * 16-byte aligned.
+ */
+moegg_status_t moegg_combine_backward(const void* dout, const void* Y, const float* weights, const int32_t* row_of,
+                                      void* dY, void* dY_scale, float* d_weights, int T, int k, int N,
+                                      int64_t rows_total, moegg_dtype_t dtype, void* stream);
+
+/*
+ * SwiGLU that keeps its input in 8 bits, for training: the first projection is
+ * run as a plain grouped GEMM to GU, and this call makes H for the down
+ * projection and the checkpoint that the backward pass reads (half of GU's
+ * bytes), in one pass.
+ *   GU       bf16 [rows_total, 2I], gate and up columns in the order of W1's
+ *            rows (blocks of 16, see moegg_grouped_gemm_swiglu_scheduled).
+ *   H        silu(g) * u [rows_total, I] in fp32, where a sigmoid(g) below 2^-126
+ *            (g < -87.3) is 0, stored as the down projection
+ *            takes it: MOEGG_BF16 (H_scale NULL), or e4m3 codes with fp32 1x128
+ *            scales [rows_total, I/128] (MOEGG_FP8_E4M3) or [I/128, rows_total]
+ *            (MOEGG_FP8_E4M3_SCALE_KM).
+ *   ckpt     e4m3 [rows_total, 2I], ckpt_scale fp32 [rows_total, 2I/128]: GU's
+ *            codes and 1x128 scales, as moegg_dispatch quantizes.
+ *   m_sizes  int32 [G]: the first sum_e max(m_e, 0) rows (at most rows_total) are
+ *            read and written; the others keep their contents.  Segments lie
+ *            back to back (seg_align 1), as in the K-grouped calls.
+ * I % 128 == 0; GU, H and ckpt 16-byte aligned, scales 4.
+ */
+moegg_status_t moegg_swiglu_checkpoint(const void* GU, const int32_t* m_sizes, void* H, void* H_scale, void* ckpt,
+                                       float* ckpt_scale, int G, int64_t rows_total, int I, moegg_dtype_t dtype,
+                                       void* stream);
+
+/*
+ * Backward pass of SwiGLU from the checkpoint, bf16: dGU bf16 [rows_total, 2I]
+ * (gate and up columns in GU's order) and H again, bf16 [rows_total, I], for
+ * the weight gradients.  With g, u the checkpoint's values and s = sigmoid(g)
+ * (0 below 2^-126, as in the forward call):
+ *     d_gate = dH * u * s * (1 + g * (1 - s)),  d_up = dH * g * s,  h = g * s * u.
+ * dH bf16 [rows_total, I].  Rows and constraints as for the forward call.
+ */
+moegg_status_t moegg_swiglu_checkpoint_backward(const void* dH, const int32_t* m_sizes, const void* ckpt,
+                                                const float* ckpt_scale, void* dGU, void* H, int G,
+                                                int64_t rows_total, int I, void* stream);
+
+/*
+ * The same for an fp8 layer, with the operands of both of the projection's
+ * gradients from one pass over the checkpoint:
+ *   dGU, dGU_scale      e4m3 [rows_total, 2I] with fp32 1x128 scales
+ *                       ([rows_total, 2I/128], or [2I/128, rows_total] with
+ *                       MOEGG_FP8_E4M3_SCALE_KM): the input gradient's product.
+ *   dGU_k, dGU_k_scale  the same gradient as e4m3 [rows_total, 2I] with one
+ *                       scale per column and token group, [scale_groups, 2I]:
+ *                       fp32, or E8M0 bytes when k_e8m0 is not 0 -- the operand
+ *                       of moegg_grouped_gemm_k_grouped_fp8 / _e8m0, whose
+ *                       token groups these are.
+ *   H_k, H_k_scale      H likewise, [rows_total, I] and [scale_groups, I].
+ * All are quantized from fp32 values.  Scale rows of groups that do not exist
+ * keep their contents; a group at or past scale_groups (at least sum_e
+ * ceil(m_e / 128) hold them all) gets codes and no scale.
+ */
+moegg_status_t moegg_swiglu_checkpoint_backward_fp8(
+    const void* dH, const int32_t* m_sizes, const void* ckpt, const float* ckpt_scale, void* dGU, float* dGU_scale,
+    void* dGU_k, void* dGU_k_scale, void* H_k, void* H_k_scale, int G, int64_t rows_total, int I,
+    int64_t scale_groups, moegg_dtype_t dtype, int k_e8m0, void* stream);
+
+/*
+ * A saved row-major activation as the operand of the K-grouped weight
+ * gradient: X bf16 [rows_total, M] (MOEGG_BF16, X_scale NULL), or e4m3 with
+ * fp32 scales [rows_total, M/128] (MOEGG_FP8_E4M3) or [M/128, rows_total]
+ * (MOEGG_FP8_E4M3_SCALE_KM) -> X_k e4m3 [rows_total, M] with one scale per
+ * column and token group, X_k_scale [scale_groups, M], fp32 or (k_e8m0) E8M0
+ * bytes.  So the fp8 input of the forward product is what a training step
+ * keeps of it.  Values are code * scale in fp32.  Rows and token groups as
+ * above.  M % 256 == 0; X and X_k 16-byte aligned, scales 4.
+ */
+moegg_status_t moegg_checkpoint_to_k_groups(const void* X, const float* X_scale, const int32_t* m_sizes, void* X_k,
+                                            void* X_k_scale, int G, int64_t rows_total, int M, int64_t scale_groups,
+                                            moegg_dtype_t dtype, int k_e8m0, void* stream);
+
 /* Copy the stats of the last scheduled call on `ws` to the host.
  * Synchronizes `stream`. */
 moegg_status_t moegg_stats_read(const void* ws, moegg_stats_t* h_out, void* stream);

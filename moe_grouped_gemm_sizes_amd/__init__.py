@@ -3,7 +3,8 @@
 The binding only marshals arguments.  Every step of the grouped GEMM runs in
 the HIP kernels behind the C ABI declared in include/moegg.h:
   - scheduler: counts -> padding accounting + tile list;
-  - contiguous, masked and K-grouped GEMMs.
+  - contiguous, masked and K-grouped GEMMs;
+  - the layer around them: routing, token permutation, 8-bit activation checkpoints.
 PyTorch supplies device memory and the current stream.  If the library has
 not been built, `lib()` raises.  There is no CPU fallback.
 """
@@ -27,6 +28,8 @@ PANEL_CONTIGUOUS, PANEL_MASKED = 256, 128     # panel width P of the contiguous 
 FLAG_NEGATIVE_COUNT, FLAG_ROWS_OVERFLOW, FLAG_COUNT_OVER_CAP, FLAG_BAD_EXEMPLAR = 0x1, 0x2, 0x4, 0x8
 FLAG_SCALE_GROUPS = 0x10
 FLAG_SYNC_TIMEOUT = 0x20
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+LOGITS_FP32, LOGITS_BF16 = 0, 1
 Q_VALUES = (8, 16, 32, 64, 128, 256)
 BLOCK_M_PER_EXPERT = -1          # per-expert tile heights (include/moegg.h)
 
@@ -98,7 +101,7 @@ class Report:
 
 
 _lib = None
-_VP, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_VP, _I32, _I64, _SZ, _F32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 
 EXPORTS = {
     "moegg_version": (ctypes.c_int, []),
@@ -124,6 +127,18 @@ EXPORTS = {
                                                 _VP, _SZ, _VP]),
     "moegg_grouped_gemm_k_grouped_e8m0": (_I32, [_VP, _VP, _VP, _VP, _VP, _VP, _I32, _I64, _I32, _I32, _I64,
                                                  _VP, _SZ, _VP]),
+    "moegg_route_workspace_bytes": (_SZ, [_I32, _I32]),
+    "moegg_route": (_I32, [_VP, _I32, _VP, _VP, _VP, _VP, _VP, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _F32,
+                           _I64, _I32, _I32, _VP, _SZ, _VP]),
+    "moegg_route_backward": (_I32, [_VP, _I32, _VP, _VP, _VP, _I32, _I32, _I32, _I32, _I32, _F32, _VP]),
+    "moegg_dispatch": (_I32, [_VP, _VP, _VP, _VP, _I32, _I32, _I32, _I64, _I32, _VP]),
+    "moegg_combine": (_I32, [_VP, _VP, _VP, _VP, _I32, _I32, _I32, _I64, _VP]),
+    "moegg_combine_backward": (_I32, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _I32, _I32, _I64, _I32, _VP]),
+    "moegg_swiglu_checkpoint": (_I32, [_VP, _VP, _VP, _VP, _VP, _VP, _I32, _I64, _I32, _I32, _VP]),
+    "moegg_swiglu_checkpoint_backward": (_I32, [_VP, _VP, _VP, _VP, _VP, _VP, _I32, _I64, _I32, _VP]),
+    "moegg_swiglu_checkpoint_backward_fp8": (_I32, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _I64,
+                                                    _I32, _I64, _I32, _I32, _VP]),
+    "moegg_checkpoint_to_k_groups": (_I32, [_VP, _VP, _VP, _VP, _VP, _I32, _I64, _I32, _I64, _I32, _I32, _VP]),
     "moegg_stats_read": (_I32, [_VP, ctypes.POINTER(_Stats), _VP]),
     "moegg_stats_report": (_I32, [ctypes.POINTER(_Stats), ctypes.POINTER(_Report)]),
     "moegg_tile_list_read": (_I32, [_VP, ctypes.POINTER(_Tile), _I64, ctypes.POINTER(_I64), _VP]),
@@ -552,6 +567,219 @@ def grouped_gemm_k_grouped(X, dY, dW, t_sizes, ws, X_scale=None, dY_scale=None, 
     _check(lib().moegg_grouped_gemm_k_grouped_fp8(
         _p(X), _p(X_scale), _p(dY), _p(dY_scale), _p(dW), _p(t_sizes), G, T, Mw, Nw, S, _p(ws), ws.numel(),
         _stream(stream)), "moegg_grouped_gemm_k_grouped_fp8")
+
+
+# ---------------------------------------------------------------- the layer around the grouped GEMMs
+
+
+def route_workspace_bytes(T: int, E: int) -> int:
+    return int(lib().moegg_route_workspace_bytes(T, E))
+
+
+def route_workspace(T: int, E: int, device="cuda") -> torch.Tensor:
+    n = route_workspace_bytes(T, E)
+    if n == 0:
+        raise ValueError("invalid workspace request")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _logits(logits) -> Tuple[int, int, int]:
+    _need(logits, "logits", [None, None], (torch.float32, torch.bfloat16))
+    T, E = logits.shape
+    return T, E, LOGITS_BF16 if logits.dtype == torch.bfloat16 else LOGITS_FP32
+
+
+def route(logits, ids, weights, m_sizes, row_of, ws, *, rows_total: int, bias=None, score: int = SCORE_SOFTMAX,
+          n_groups: int = 1, topk_groups: int = 1, group_top: int = 1, renorm: bool = True, scale: float = 1.0,
+          seg_align: int = 1, cap: int = 0, stream=None):
+    """logits [T, E] -> ids, weights, row_of [T, k] and m_sizes [E] (see moegg.h): top-k experts by softmax or
+    sigmoid score (plus bias [E] for the choice alone), group-limited when n_groups > 1; row_of is the row of every
+    assignment in the contiguous layout of rows_total rows, or with cap > 0 in [E, cap] capacity buffers
+    (rows_total = E * cap); -1 where there is none.  ws: route_workspace(T, E)."""
+    T, E, kind = _logits(logits)
+    _need(ids, "ids", [T, None], (torch.int32,))
+    k = ids.shape[1]
+    _need(weights, "weights", [T, k], (torch.float32,))
+    _need(m_sizes, "m_sizes", [E], (torch.int32,))
+    _need(row_of, "row_of", [T, k], (torch.int32,))
+    if bias is not None:
+        _need(bias, "bias", [E], (torch.float32,))
+    _need(ws, "ws", [None], (torch.uint8,))
+    need = route_workspace_bytes(T, E)
+    if ws.numel() < need:
+        raise ValueError(f"ws: {ws.numel()} bytes, need {need} (route_workspace_bytes({T}, {E}))")
+    _one_device(logits, ids, weights, m_sizes, row_of, bias, ws)
+    _check(lib().moegg_route(_p(logits), kind, _p(bias), _p(ids), _p(weights), _p(m_sizes), _p(row_of), T, E, k,
+                             score, n_groups, topk_groups, group_top, renorm, scale, rows_total, seg_align, cap,
+                             _p(ws), ws.numel(), _stream(stream)), "moegg_route")
+
+
+def route_backward(logits, ids, d_weights, d_logits, *, score: int = SCORE_SOFTMAX, renorm: bool = True,
+                   scale: float = 1.0, stream=None):
+    """d_logits [T, E] (logits' dtype) from d_weights [T, k] and the ids that route chose (see moegg.h)."""
+    T, E, kind = _logits(logits)
+    _need(ids, "ids", [T, None], (torch.int32,))
+    k = ids.shape[1]
+    _need(d_weights, "d_weights", [T, k], (torch.float32,))
+    _need(d_logits, "d_logits", [T, E], (logits.dtype,))
+    _one_device(logits, ids, d_weights, d_logits)
+    _check(lib().moegg_route_backward(_p(logits), kind, _p(ids), _p(d_weights), _p(d_logits), T, E, k, score, renorm,
+                                      scale, _stream(stream)), "moegg_route_backward")
+
+
+def _row_operand(A, name: str, A_scale, width: int, scale_km: bool) -> Tuple[int, int]:
+    """Rows and operand type code of an expert-side operand [rows, width] or [G, cap, width] and its scales."""
+    if not isinstance(A, torch.Tensor) or A.dim() not in (2, 3):
+        raise ValueError(f"{name}: tensor [rows, width] or [G, cap, width] expected")
+    _need(A, name, [None] * (A.dim() - 1) + [width], (torch.bfloat16, _E4M3))
+    rows = A.shape[0] if A.dim() == 2 else A.shape[0] * A.shape[1]
+    if A.dtype == torch.bfloat16:
+        _none(A_scale, f"{name}_scale", "for a bf16 operand")
+        if scale_km:
+            raise ValueError("scale_km applies to e4m3 operands with fp32 scales")
+        return rows, BF16
+    if width % 128:
+        raise ValueError(f"{name}: width {width}, e4m3 operands need a multiple of 128")
+    if isinstance(A_scale, torch.Tensor) and A_scale.dtype == torch.uint8:
+        if scale_km:
+            raise ValueError("scale_km applies to e4m3 operands with fp32 scales")
+        _need(A_scale, f"{name}_scale", [width // 128, rows], (torch.uint8,))
+        return rows, FP8_E4M3_E8M0
+    _need(A_scale, f"{name}_scale", [width // 128, rows] if scale_km else [*A.shape[:-1], width // 128],
+          (torch.float32,))
+    return rows, FP8_E4M3_SCALE_KM if scale_km else FP8_E4M3
+
+
+def dispatch(x, row_of, A, A_scale=None, *, scale_km: bool = False, stream=None):
+    """A[row_of[t, j]] = x[t] (see moegg.h).  x bf16 [T, K]; A bf16 or e4m3, [rows, K] or [G, cap, K], with the
+    scales of the grouped GEMM that reads it: fp32 [rows, K/128] ([G, cap, K/128]), [K/128, rows] (scale_km), or
+    uint8 E8M0 bytes [K/128, rows]."""
+    _need(x, "x", [None, None], (torch.bfloat16,))
+    T, K = x.shape
+    _need(row_of, "row_of", [T, None], (torch.int32,))
+    rows, code = _row_operand(A, "A", A_scale, K, scale_km)
+    _one_device(x, row_of, A, A_scale)
+    _check(lib().moegg_dispatch(_p(x), _p(row_of), _p(A), _p(A_scale), T, row_of.shape[1], K, rows, code,
+                                _stream(stream)), "moegg_dispatch")
+
+
+def _expert_rows(Y, N: int) -> int:
+    if not isinstance(Y, torch.Tensor) or Y.dim() not in (2, 3):
+        raise ValueError("Y: tensor [rows, N] or [G, cap, N] expected")
+    _need(Y, "Y", [None] * (Y.dim() - 1) + [N], (torch.bfloat16,))
+    return Y.shape[0] if Y.dim() == 2 else Y.shape[0] * Y.shape[1]
+
+
+def combine(Y, row_of, out, weights=None, *, stream=None):
+    """out[t] = sum_j weights[t, j] * Y[row_of[t, j]] (see moegg.h); weights None: all 1, which is also dispatch's
+    backward pass.  Y bf16 [rows, N] or [G, cap, N], out bf16 [T, N], weights fp32 [T, k]."""
+    _need(out, "out", [None, None], (torch.bfloat16,))
+    T, N = out.shape
+    _need(row_of, "row_of", [T, None], (torch.int32,))
+    rows = _expert_rows(Y, N)
+    if weights is not None:
+        _need(weights, "weights", list(row_of.shape), (torch.float32,))
+    _one_device(Y, row_of, out, weights)
+    _check(lib().moegg_combine(_p(Y), _p(row_of), _p(weights), _p(out), T, row_of.shape[1], N, rows,
+                               _stream(stream)), "moegg_combine")
+
+
+def combine_backward(dout, Y, weights, row_of, dY, d_weights, dY_scale=None, *, scale_km: bool = False, stream=None):
+    """dY[row_of[t, j]] = weights[t, j] * dout[t] in dY's operand format (as dispatch's A), and d_weights[t, j] =
+    <Y[row_of[t, j]], dout[t]> (see moegg.h)."""
+    _need(dout, "dout", [None, None], (torch.bfloat16,))
+    T, N = dout.shape
+    _need(row_of, "row_of", [T, None], (torch.int32,))
+    _need(weights, "weights", list(row_of.shape), (torch.float32,))
+    _need(d_weights, "d_weights", list(row_of.shape), (torch.float32,))
+    rows, code = _row_operand(dY, "dY", dY_scale, N, scale_km)
+    if _expert_rows(Y, N) != rows:
+        raise ValueError(f"Y: shape {list(Y.shape)}, expected {rows} rows as dY")
+    _one_device(dout, Y, weights, row_of, dY, d_weights, dY_scale)
+    _check(lib().moegg_combine_backward(_p(dout), _p(Y), _p(weights), _p(row_of), _p(dY), _p(dY_scale), _p(d_weights),
+                                        T, row_of.shape[1], N, rows, code, _stream(stream)), "moegg_combine_backward")
+
+
+def _no_e8m0(code: int, name: str):
+    if code == FP8_E4M3_E8M0:
+        raise ValueError(f"{name}: fp32 scales expected")
+
+
+def _token_group_scales(X_scale, name: str, width: int, groups: Optional[int] = None, dtype=None) -> int:
+    _need(X_scale, name, [groups, width], (torch.float32, torch.uint8) if dtype is None else (dtype,))
+    return X_scale.shape[0]
+
+
+def swiglu_checkpoint(GU, m_sizes, H, ckpt, ckpt_scale, H_scale=None, *, scale_km: bool = False, stream=None):
+    """H = silu(g) * u of GU bf16 [rows, 2I] (columns in interleave_gate_up's order), and GU kept as e4m3 ckpt
+    [rows, 2I] with fp32 ckpt_scale [rows, 2I/128] (see moegg.h).  H bf16 [rows, I], or e4m3 with H_scale fp32
+    [rows, I/128] ([I/128, rows] with scale_km)."""
+    _need(H, "H", [None, None], (torch.bfloat16, _E4M3))
+    rows, I = H.shape
+    _, code = _row_operand(H, "H", H_scale, I, scale_km)
+    _no_e8m0(code, "H_scale")
+    _need(GU, "GU", [rows, 2 * I], (torch.bfloat16,))
+    _need(ckpt, "ckpt", [rows, 2 * I], (_E4M3,))
+    _need(ckpt_scale, "ckpt_scale", [rows, 2 * I // 128], (torch.float32,))
+    _counts(m_sizes, "m_sizes")
+    _one_device(GU, m_sizes, H, ckpt, ckpt_scale, H_scale)
+    _check(lib().moegg_swiglu_checkpoint(_p(GU), _p(m_sizes), _p(H), _p(H_scale), _p(ckpt), _p(ckpt_scale),
+                                         m_sizes.numel(), rows, I, code, _stream(stream)), "moegg_swiglu_checkpoint")
+
+
+def swiglu_checkpoint_backward(dH, m_sizes, ckpt, ckpt_scale, dGU, H, *, stream=None):
+    """dGU bf16 [rows, 2I] and H bf16 [rows, I] again, from dH bf16 [rows, I] and the checkpoint (see moegg.h)."""
+    _need(dH, "dH", [None, None], (torch.bfloat16,))
+    rows, I = dH.shape
+    _need(ckpt, "ckpt", [rows, 2 * I], (_E4M3,))
+    _need(ckpt_scale, "ckpt_scale", [rows, 2 * I // 128], (torch.float32,))
+    _need(dGU, "dGU", [rows, 2 * I], (torch.bfloat16,))
+    _need(H, "H", [rows, I], (torch.bfloat16,))
+    _counts(m_sizes, "m_sizes")
+    _one_device(dH, m_sizes, ckpt, ckpt_scale, dGU, H)
+    _check(lib().moegg_swiglu_checkpoint_backward(_p(dH), _p(m_sizes), _p(ckpt), _p(ckpt_scale), _p(dGU), _p(H),
+                                                  m_sizes.numel(), rows, I, _stream(stream)),
+           "moegg_swiglu_checkpoint_backward")
+
+
+def swiglu_checkpoint_backward_fp8(dH, m_sizes, ckpt, ckpt_scale, dGU, dGU_scale, dGU_k, dGU_k_scale, H_k, H_k_scale,
+                                   *, scale_km: bool = False, stream=None):
+    """The operands of both gradients' products from dH bf16 [rows, I] and the checkpoint (see moegg.h): dGU e4m3
+    [rows, 2I] with fp32 dGU_scale [rows, 2I/128] ([2I/128, rows] with scale_km); dGU_k e4m3 [rows, 2I] and H_k
+    e4m3 [rows, I] with scales per token group, [S, 2I] and [S, I], fp32 or uint8 E8M0 bytes (k_scale_groups)."""
+    _need(dH, "dH", [None, None], (torch.bfloat16,))
+    rows, I = dH.shape
+    _need(ckpt, "ckpt", [rows, 2 * I], (_E4M3,))
+    _need(ckpt_scale, "ckpt_scale", [rows, 2 * I // 128], (torch.float32,))
+    _need(dGU, "dGU", [rows, 2 * I], (_E4M3,))
+    _, code = _row_operand(dGU, "dGU", dGU_scale, 2 * I, scale_km)
+    _no_e8m0(code, "dGU_scale")
+    _need(dGU_k, "dGU_k", [rows, 2 * I], (_E4M3,))
+    _need(H_k, "H_k", [rows, I], (_E4M3,))
+    S = _token_group_scales(dGU_k_scale, "dGU_k_scale", 2 * I)
+    _token_group_scales(H_k_scale, "H_k_scale", I, S, dGU_k_scale.dtype)
+    _counts(m_sizes, "m_sizes")
+    _one_device(dH, m_sizes, ckpt, ckpt_scale, dGU, dGU_scale, dGU_k, dGU_k_scale, H_k, H_k_scale)
+    _check(lib().moegg_swiglu_checkpoint_backward_fp8(
+        _p(dH), _p(m_sizes), _p(ckpt), _p(ckpt_scale), _p(dGU), _p(dGU_scale), _p(dGU_k), _p(dGU_k_scale), _p(H_k),
+        _p(H_k_scale), m_sizes.numel(), rows, I, S, code, dGU_k_scale.dtype == torch.uint8, _stream(stream)),
+        "moegg_swiglu_checkpoint_backward_fp8")
+
+
+def checkpoint_to_k_groups(X, m_sizes, X_k, X_k_scale, X_scale=None, *, scale_km: bool = False, stream=None):
+    """A saved activation X [rows, M] (bf16, or e4m3 with fp32 scales [rows, M/128], [M/128, rows] with scale_km) as
+    an operand of grouped_gemm_k_grouped: X_k e4m3 [rows, M] with X_k_scale [S, M], fp32 or uint8 E8M0 (see moegg.h)."""
+    _need(X, "X", [None, None], (torch.bfloat16, _E4M3))
+    rows, M = X.shape
+    _, code = _row_operand(X, "X", X_scale, M, scale_km)
+    _no_e8m0(code, "X_scale")
+    _need(X_k, "X_k", [rows, M], (_E4M3,))
+    S = _token_group_scales(X_k_scale, "X_k_scale", M)
+    _counts(m_sizes, "m_sizes")
+    _one_device(X, X_scale, m_sizes, X_k, X_k_scale)
+    _check(lib().moegg_checkpoint_to_k_groups(_p(X), _p(X_scale), _p(m_sizes), _p(X_k), _p(X_k_scale),
+                                              m_sizes.numel(), rows, M, S, code, X_k_scale.dtype == torch.uint8,
+                                              _stream(stream)), "moegg_checkpoint_to_k_groups")
 
 
 def stats_read(ws: torch.Tensor, stream=None) -> Stats:

@@ -14,7 +14,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoegg.so")
-SOURCES = ["api.hip", "sched.hip", "gemm.hip"]
+SOURCES = ["api.hip", "layer_api.hip", "sched.hip", "gemm.hip", "route.hip", "permute.hip", "checkpoint.hip"]
 ARCH = "gfx950"
 
 # Packed fp32 VALU ops are switched off for all device code.

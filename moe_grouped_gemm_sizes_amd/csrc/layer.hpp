@@ -1,0 +1,236 @@
+// layer.hpp -- what the layer operators around the grouped GEMMs share: wave
+// reductions, e4m3 quantization by groups, and the launchers that the C ABI
+// (layer_api.hip) calls (route.hip, permute.hip, checkpoint.hip).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/moegg.h"
+
+namespace moegg {
+
+constexpr int kRouteMaxExperts = 1024;   // experts a wave holds in registers, 16 a lane
+constexpr int kRouteMaxTopK = 32;
+constexpr int kRouteMaxTiles = 256;      // token tiles of a routing call (one workgroup each)
+constexpr int kRouteMaxTokens = kRouteMaxTiles * 65520;   // a tile's counts are 16 bits
+constexpr int kGroup = 128;              // elements of one quantization group
+
+struct RouteArgs {
+    const void* logits;                  // fp32 or bf16 [T, E]
+    const float* bias;                   // [E] or NULL
+    int32_t* ids;                        // [T, k]
+    float* weights;                      // [T, k]
+    int32_t* m_sizes;                    // [E]
+    int32_t* row_of;                     // [T, k]
+    uint16_t* tile_counts;               // [tiles, E rounded up to 2]: assignments of each token tile
+    int T, E, k;
+    int bf16;                            // logits' type
+    int sigmoid, renorm;
+    int n_groups, topk_groups, group_top;
+    float scale;
+    int64_t rows_total;
+    int seg_align, cap;
+    int tile_tokens;                     // tokens of one workgroup
+};
+
+struct RouteBackwardArgs {
+    const void* logits;
+    const int32_t* ids;
+    const float* d_weights;
+    void* d_logits;                      // logits' type
+    int T, E, k, bf16, sigmoid, renorm;
+    float scale;
+};
+
+// How a row-major operand is stored (moegg_dtype_t of the call that will read it).
+enum OperandFormat { kBf16 = 0, kRows = 1, kKm = 2, kE8m0 = 3 };
+
+struct PermuteArgs {
+    const void* x;                       // dispatch: bf16 [T, W]; combine: Y bf16 [rows, W]; backward: dout [T, W]
+    const void* Y;                       // combine backward: bf16 [rows, W]
+    const float* weights;                // [T, k] or NULL
+    const int32_t* row_of;               // [T, k]
+    void* out;                           // dispatch: A; combine: out; backward: dY
+    void* scale;                         // of an e4m3 output
+    float* d_weights;                    // combine backward: [T, k]
+    int T, k, W;
+    int rows;                            // rows of the expert side
+    OperandFormat fmt;
+};
+
+struct CheckpointArgs {
+    const void* in;                      // forward: GU bf16; backward: dH bf16; k groups: X
+    const float* in_scale;               // k groups: scales of X (NULL: bf16)
+    const int32_t* m_sizes;              // [G]
+    uint8_t* ckpt;                       // e4m3 [rows, 2I]
+    float* ckpt_scale;                   // [rows, 2I / 128]
+    void* row_out;                       // forward: H; backward: dGU
+    void* row_scale;
+    void* H;                             // bf16 backward: H
+    uint8_t* k_out;                      // dGU or X by token groups
+    void* k_scale;
+    uint8_t* hk_out;                     // H by token groups
+    void* hk_scale;
+    int G, rows, W;                      // W: I, or the width of X
+    int64_t scale_groups;
+    OperandFormat fmt;                   // of row_out; k groups: of X
+    int k_e8m0;                          // token-group scales are E8M0 bytes
+};
+
+hipError_t launch_route(const RouteArgs& a, hipStream_t s);
+hipError_t launch_route_backward(const RouteBackwardArgs& a, hipStream_t s);
+hipError_t launch_dispatch(const PermuteArgs& a, hipStream_t s);
+hipError_t launch_combine(const PermuteArgs& a, hipStream_t s);
+hipError_t launch_combine_backward(const PermuteArgs& a, hipStream_t s);
+hipError_t launch_swiglu_checkpoint(const CheckpointArgs& a, hipStream_t s);
+hipError_t launch_swiglu_checkpoint_backward(const CheckpointArgs& a, hipStream_t s);
+hipError_t launch_swiglu_checkpoint_backward_fp8(const CheckpointArgs& a, hipStream_t s);
+hipError_t launch_checkpoint_to_k_groups(const CheckpointArgs& a, hipStream_t s);
+
+// Tokens of one workgroup of a routing call: a multiple of 16, at most 256 workgroups.
+inline int route_tile_tokens(int T) {
+    const int t = (T + kRouteMaxTiles - 1) / kRouteMaxTiles;
+    return t <= 16 ? 16 : (t + 15) / 16 * 16;
+}
+
+#ifdef __HIPCC__
+
+// ----------------------------------------------------------------- cross-lane
+
+// Lane exchange by DPP: CTRL is quad_perm, row_shr, row_ror, row_bcast, ...
+// (16-lane rows); lanes with no source get `old`.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t old, uint32_t x) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)x, CTRL, 0xF, 0xF, false);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp_f(float old, float x) {
+    return __uint_as_float(dpp<CTRL>(__float_as_uint(old), __float_as_uint(x)));
+}
+constexpr int DPP_XOR1 = 0xB1;            // quad_perm [1,0,3,2]
+constexpr int DPP_XOR2 = 0x4E;            // quad_perm [2,3,0,1]
+constexpr int DPP_HALF_MIRROR = 0x141;    // lane i of 8 <-> 7 - i
+constexpr int DPP_MIRROR = 0x140;         // lane i of 16 <-> 15 - i
+constexpr int DPP_SHR = 0x110;            // + n: row_shr by n
+constexpr int DPP_BCAST15 = 0x142, DPP_BCAST31 = 0x143;
+
+// Maximum over each aligned group of 8 or 16 lanes, in every lane of it.
+__device__ __forceinline__ float max8(float v) {
+    v = fmaxf(v, dpp_f<DPP_XOR1>(v, v));
+    v = fmaxf(v, dpp_f<DPP_XOR2>(v, v));
+    return fmaxf(v, dpp_f<DPP_HALF_MIRROR>(v, v));
+}
+__device__ __forceinline__ float max16(float v) {
+    v = max8(v);
+    return fmaxf(v, dpp_f<DPP_MIRROR>(v, v));
+}
+
+// Wave-wide reductions: an inclusive scan by DPP whose last lane holds the
+// result, handed to every lane as a scalar.
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+    v = max(v, dpp<DPP_SHR + 1>(0, v));
+    v = max(v, dpp<DPP_SHR + 2>(0, v));
+    v = max(v, dpp<DPP_SHR + 4>(0, v));
+    v = max(v, dpp<DPP_SHR + 8>(0, v));
+    v = max(v, dpp<DPP_BCAST15>(0, v));
+    v = max(v, dpp<DPP_BCAST31>(0, v));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ float wave_max(float v) {
+    constexpr float lo = -__builtin_inff();
+    v = fmaxf(v, dpp_f<DPP_SHR + 1>(lo, v));
+    v = fmaxf(v, dpp_f<DPP_SHR + 2>(lo, v));
+    v = fmaxf(v, dpp_f<DPP_SHR + 4>(lo, v));
+    v = fmaxf(v, dpp_f<DPP_SHR + 8>(lo, v));
+    v = fmaxf(v, dpp_f<DPP_BCAST15>(lo, v));
+    v = fmaxf(v, dpp_f<DPP_BCAST31>(lo, v));
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+// row_bcast hands a row's sum to the next rows only: with bound lanes reading
+// 0, lane 63 sums rows 0..3 in a fixed order.
+__device__ __forceinline__ float wave_sum(float v) {
+    v += dpp_f<DPP_SHR + 1>(0.f, v);
+    v += dpp_f<DPP_SHR + 2>(0.f, v);
+    v += dpp_f<DPP_SHR + 4>(0.f, v);
+    v += dpp_f<DPP_SHR + 8>(0.f, v);
+    v += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), DPP_BCAST15, 0xA, 0xF, false));
+    v += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), DPP_BCAST31, 0xC, 0xF, false));
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+
+// ----------------------------------------------------------------- numbers
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+// the same, at any even address (rows of odd width); one load or store all the same
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+
+__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+
+// 1 / (1 + e^-x) by the hardware's exp2 and reciprocal (1 ulp each).  The
+// rounded product x log2 e costs |x| 2^-24 relative at most, 1e-6 at |x| = 16;
+// its users round the result to 8 or 4 bits.  Below 2^-126 the reciprocal is 0.
+__device__ __forceinline__ float sigmoid_fast(float x) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * -1.44269504f));
+}
+
+// Four fp32 -> four e4m3 codes, round to nearest even, |x| <= 448 (NaN: code 0x7F).
+__device__ __forceinline__ uint32_t e4m3_x4(float a, float b, float c, float d) {
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
+}
+// Four e4m3 codes -> fp32.
+__device__ __forceinline__ void e4m3_to_f32(uint32_t v, float* f) {
+    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)v, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)v, true);
+    f[0] = lo.x;
+    f[1] = lo.y;
+    f[2] = hi.x;
+    f[3] = hi.y;
+}
+
+// One group's scale amax / 448 (1 where that is 0; POW2: the smallest power of
+// two that is at least it, from 2^-126 up, as value and E8M0 byte) and inv,
+// what values are multiplied with to become codes.  x * (1 / s) is within 1.5
+// ulp of x / s: it moves a code only where x / s is that near a rounding border.
+struct GroupScale {
+    float s, inv;
+    uint32_t byte;
+};
+template <bool POW2>
+__device__ __forceinline__ GroupScale group_scale(float amax) {
+    GroupScale g;
+    g.s = amax / 448.f;
+    if (!(g.s > 0.f)) g.s = 1.f;
+    g.byte = 0;
+    if (POW2) {
+        const uint32_t b = __float_as_uint(g.s);
+        const uint32_t e = max((b >> 23) + ((b & 0x7FFFFFu) != 0u), 1u);   // amax finite: at most 247; inf: 255
+        g.byte = e;
+        g.s = __uint_as_float(e << 23);
+        g.inv = e == 255u ? 0.f : __uint_as_float((254u - e) << 23);
+    } else {
+        g.inv = 1.f / g.s;
+    }
+    return g;
+}
+
+// Code of one value whose group's scale s is so small that 1 / s may overflow
+// and s itself be rounded coarsely: a division, and the clamp that this needs.
+__device__ __forceinline__ float tiny_quotient(float x, float s) {
+    const float q = x / s;
+    return q != q ? q : fminf(fmaxf(q, -448.f), 448.f);
+}
+constexpr float kTinyScale = 0x1p-100f;
+
+// Four values of one group -> their codes.
+__device__ __forceinline__ uint32_t quantize_x4(float a, float b, float c, float d, const GroupScale& g) {
+    if (g.s < kTinyScale)
+        return e4m3_x4(tiny_quotient(a, g.s), tiny_quotient(b, g.s), tiny_quotient(c, g.s), tiny_quotient(d, g.s));
+    return e4m3_x4(a * g.inv, b * g.inv, c * g.inv, d * g.inv);
+}
+
+#endif  // __HIPCC__
+
+}  // namespace moegg

@@ -16,6 +16,7 @@ Parts:
   histogram matched against an exemplar table, with hysteresis).
 - choice.py: the integer cost rule that picks the tile height for block_m = 0.
 - mlp.py: the expert MLP, L1 projection -> SwiGLU -> L2 projection, in fp64.
+- layer.py: the operators around the GEMMs: routing, token permutation, SwiGLU and its gradient, scale groups.
 
 Every function states the page and section it follows.  Parity pins live in
 tests/test_oracle_*.py and tests/golden/.
@@ -26,3 +27,4 @@ from . import fp4  # noqa: F401
 from . import select  # noqa: F401
 from . import choice  # noqa: F401
 from . import mlp  # noqa: F401
+from . import layer  # noqa: F401
