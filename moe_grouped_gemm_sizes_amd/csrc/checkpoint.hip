@@ -4,12 +4,9 @@
 // of the K-grouped weight gradient.
 //
 // All are bound by memory.  Gate and up columns alternate in blocks of 16 (the
-// row order of W1), so 16 lanes take one row's unit of 256 gate/up columns =
-// 128 columns of H: lane 2q + h has gate columns 32q + 8h .. + 7, the up columns
-// 16 further on, and columns 16q + 8h .. + 7 of H.  A 128-column group of the
-// checkpoint is 8 lanes and a group of H all 16, so each amax is three or four
-// DPP steps; codes of neighbouring lanes are exchanged so that each lane stores
-// 16 contiguous bytes.
+// row order of W1).  A lane computes 8 columns of H from 8 gate columns and the
+// 8 up columns 16 further on; lanes exchange halves by DPP so that every load
+// and store is 16 contiguous bytes a lane and whole lines an instruction.
 #include <hip/hip_runtime.h>
 
 #include "device.hpp"
@@ -18,23 +15,18 @@
 namespace moegg {
 
 constexpr int kThreads = 256;
-constexpr int kXcds = 8;
 constexpr int kUnit = 256;                // gate/up columns of 16 lanes
 
 // Codes of 8 gate and 8 up columns <-> 16 contiguous codes of a unit at lane * 16.
 __device__ __forceinline__ u32x4 join_codes(u32x2 g, u32x2 u, bool odd) {
     const u32x2 send = odd ? g : u;
-    u32x2 got;
-    got.x = dpp<DPP_XOR1>(0, send.x);
-    got.y = dpp<DPP_XOR1>(0, send.y);
+    const u32x2 got = {lane_of<DPP_XOR1>(send.x), lane_of<DPP_XOR1>(send.y)};
     return odd ? u32x4{got.x, got.y, u.x, u.y} : u32x4{g.x, g.y, got.x, got.y};
 }
 __device__ __forceinline__ void split_codes(u32x4 c, bool odd, u32x2& g, u32x2& u) {
     const u32x2 lo = {c.x, c.y}, hi = {c.z, c.w};
     const u32x2 send = odd ? lo : hi;
-    u32x2 got;
-    got.x = dpp<DPP_XOR1>(0, send.x);
-    got.y = dpp<DPP_XOR1>(0, send.y);
+    const u32x2 got = {lane_of<DPP_XOR1>(send.x), lane_of<DPP_XOR1>(send.y)};
     g = odd ? got : lo;
     u = odd ? hi : got;
 }
@@ -51,9 +43,6 @@ __device__ __forceinline__ u32x4 pack8(const float* f) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
     return v;
-}
-__device__ __forceinline__ u32x2 quantize8(const float* f, const GroupScale& g) {
-    return u32x2{quantize_x4(f[0], f[1], f[2], f[3], g), quantize_x4(f[4], f[5], f[6], f[7], g)};
 }
 __device__ __forceinline__ float amax8(const float* f, float m) {
 #pragma unroll
@@ -78,41 +67,71 @@ __device__ __forceinline__ int valid_rows(const int32_t* m_sizes, int G, int row
     return __builtin_amdgcn_readfirstlane((int)sum);
 }
 
-// Units of this workgroup: XCD x works on the x-th eighth of the rows, each of
-// its workgroups on a run of them.
-struct UnitRange {
-    int64_t at, end;
-};
-__device__ __forceinline__ UnitRange unit_range(int64_t units) {
-    const int64_t order = (int64_t)(blockIdx.x % kXcds) * (gridDim.x / kXcds) + blockIdx.x / kXcds;
-    const int64_t per = ((units + gridDim.x - 1) / gridDim.x + 15) / 16 * 16;
-    return {min(units, order * per) + (threadIdx.x >> 4), min(units, (order + 1) * per)};
-}
+constexpr int kRowRun = 32;               // of the row-wise kernels: 16 units a workgroup
 
 // ----------------------------------------------------------------- forward
+
+// A lane's part of a unit of 256 gate/up columns: half `odd` (8 gate and 8 up
+// columns) of its 32-column block `block`.  Lanes 4q .. 4q + 3 have blocks q and
+// q + 4, one in each 128-column half of the unit.
+struct UnitLane {
+    int l16;
+    bool odd, upper;                                     // upper: block q + 4
+    int block;
+    __device__ __forceinline__ UnitLane()
+        : l16(threadIdx.x & 15), odd(l16 & 1), upper(l16 & 2), block((upper ? 4 : 0) + (l16 >> 2)) {}
+    __device__ __forceinline__ int codes() const { return block * 32 + odd * 16; }   // 16 bytes of the unit
+    __device__ __forceinline__ int h() const { return block * 16 + odd * 8; }         // 8 columns of H
+};
+// 16-byte pieces l16 of a unit's two halves <-> gate and up columns of the lane's block (bf16).
+__device__ __forceinline__ u32x4 from_lane2(u32x4 v) {
+    return u32x4{lane_of<DPP_XOR2>(v.x), lane_of<DPP_XOR2>(v.y), lane_of<DPP_XOR2>(v.z), lane_of<DPP_XOR2>(v.w)};
+}
+__device__ __forceinline__ void split_halves(u32x4 first, u32x4 second, bool upper, u32x4& gate, u32x4& up) {
+    const u32x4 got = from_lane2(upper ? first : second);
+    gate = upper ? got : first;
+    up = upper ? second : got;
+}
+__device__ __forceinline__ void join_halves(u32x4 gate, u32x4 up, bool upper, u32x4& first, u32x4& second) {
+    const u32x4 got = from_lane2(upper ? gate : up);
+    first = upper ? got : gate;
+    second = upper ? up : got;
+}
+// Maximum over the 8 lanes that share a 128-column half, of a float that is not negative.
+__device__ __forceinline__ float max_half(float f) {
+    uint32_t v = __float_as_uint(f);
+    v = max(v, lane_of<DPP_XOR1>(v));
+    v = max(v, lane_of<DPP_ROR4>(v));
+    return __uint_as_float(max(v, lane_of<DPP_ROR8>(v)));
+}
 
 template <OperandFormat FMT>
 __global__ __launch_bounds__(kThreads) void swiglu_checkpoint_kernel(CheckpointArgs a) {
     const int upr = a.W / 128;                           // units of a row
-    const UnitRange r = unit_range((int64_t)valid_rows(a.m_sizes, a.G, a.rows) * upr);
-    const int l16 = threadIdx.x & 15;
-    const bool odd = l16 & 1;
-    for (int64_t u = r.at; u < r.end; u += kThreads / 16) {
-        const uint16_t* p = (const uint16_t*)a.in + u * kUnit + 32 * (l16 >> 1) + 8 * odd;
-        float g[8], v[8], h[8];
-        unpack8(*(const u32x4*)p, g);
-        unpack8(*(const u32x4*)(p + 16), v);
-        const GroupScale cs = group_scale<false>(max8(amax8(v, amax8(g, 0.f))));
-        *(u32x4*)(a.ckpt + u * kUnit + l16 * 16) = join_codes(quantize8(g, cs), quantize8(v, cs), odd);
-        if ((l16 & 7) == 0) a.ckpt_scale[u * 2 + (l16 >> 3)] = cs.s;
+    const UnitLane at;
+    const int64_t u = work_position<kRowRun>() * (kThreads / 16) + (threadIdx.x >> 4);
+    if (u < (int64_t)valid_rows(a.m_sizes, a.G, a.rows) * upr) {
+        const uint16_t* p = (const uint16_t*)a.in + u * kUnit + at.l16 * 8;
+        u32x4 gate, up;
+        split_halves(load_once((const u32x4*)p), load_once((const u32x4*)(p + 128)), at.upper, gate, up);
+        float gu[16], h[8];                              // 8 of gate, 8 of up
+        unpack8(gate, gu);
+        unpack8(up, gu + 8);
+        const GroupScale cs = group_scale<false>(max_half(amax8(gu + 8, amax8(gu, 0.f))));
+        uint32_t q[4];
+        quantize<16>(gu, cs, q);
+        store_once(a.ckpt + u * kUnit + at.codes(), join_codes(u32x2{q[0], q[1]}, u32x2{q[2], q[3]}, at.odd));
+        if ((at.l16 & 13) == 0) a.ckpt_scale[u * 2 + at.upper] = cs.s;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = g[i] * sigmoid_fast(g[i]) * v[i];
+        for (int i = 0; i < 8; ++i) h[i] = gu[i] * sigmoid_fast(gu[i]) * gu[8 + i];
         if (FMT == kBf16) {
-            *(u32x4*)((uint16_t*)a.row_out + u * 128 + l16 * 8) = pack8(h);
+            store_once((uint16_t*)a.row_out + u * 128 + at.h(), pack8(h));
         } else {
             const GroupScale hs = group_scale<false>(max16(amax8(h, 0.f)));
-            *(u32x2*)((uint8_t*)a.row_out + u * 128 + l16 * 8) = quantize8(h, hs);
-            if (l16 == 0) {
+            uint32_t hq[2];
+            quantize<8>(h, hs, hq);
+            store_once((uint8_t*)a.row_out + u * 128 + at.h(), u32x2{hq[0], hq[1]});
+            if (at.l16 == 0) {
                 const int64_t row = u / upr;
                 store_scale<FMT>(a.row_scale, row, (int)(u - row * upr), upr, a.rows, hs.s);
             }
@@ -147,19 +166,20 @@ __device__ __forceinline__ void swiglu_grad8(u32x4 codes, float scale, u32x4 dh,
 
 __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(CheckpointArgs a) {
     const int upr = a.W / 128;
-    const UnitRange r = unit_range((int64_t)valid_rows(a.m_sizes, a.G, a.rows) * upr);
-    const int l16 = threadIdx.x & 15;
-    const bool odd = l16 & 1;
-    for (int64_t u = r.at; u < r.end; u += kThreads / 16) {
-        const u32x4 codes = *(const u32x4*)(a.ckpt + u * kUnit + l16 * 16);
-        const u32x4 dh = *(const u32x4*)((const uint16_t*)a.in + u * 128 + l16 * 8);
-        const float scale = a.ckpt_scale[u * 2 + (l16 >> 3)];
+    const UnitLane at;
+    const int64_t u = work_position<kRowRun>() * (kThreads / 16) + (threadIdx.x >> 4);
+    if (u < (int64_t)valid_rows(a.m_sizes, a.G, a.rows) * upr) {
+        const u32x4 codes = load_once((const u32x4*)(a.ckpt + u * kUnit + at.codes()));
+        const u32x4 dh = load_once((const u32x4*)((const uint16_t*)a.in + u * 128 + at.h()));
+        const float scale = a.ckpt_scale[u * 2 + at.upper];
         float dg[8], du[8], h[8];
-        swiglu_grad8(codes, scale, dh, odd, dg, du, h);
-        uint16_t* p = (uint16_t*)a.row_out + u * kUnit + 32 * (l16 >> 1) + 8 * odd;
-        *(u32x4*)p = pack8(dg);
-        *(u32x4*)(p + 16) = pack8(du);
-        *(u32x4*)((uint16_t*)a.H + u * 128 + l16 * 8) = pack8(h);
+        swiglu_grad8(codes, scale, dh, at.odd, dg, du, h);
+        u32x4 first, second;
+        join_halves(pack8(dg), pack8(du), at.upper, first, second);
+        uint16_t* p = (uint16_t*)a.row_out + u * kUnit + at.l16 * 8;
+        store_once(p, first);
+        store_once(p + 128, second);
+        store_once((uint16_t*)a.H + u * 128 + at.h(), pack8(h));
     }
 }
 
@@ -226,15 +246,15 @@ __device__ __forceinline__ void reduce_rows(const float (&v)[N], float (&out)[N 
     }
 }
 
-// Column scales of a tile: maxima of WAVES waves in red -> scale and inverse in
-// LDS, scale stored to k_scale.  tiny: some scale needs tiny_quotient.
+// A column's scale: pre and inverse into LDS, the scale itself to k_scale.
+// tiny: some column has a pre that is not 1.
 template <bool E8M0>
-__device__ __forceinline__ void column_scale(float amax, float* s_out, float* inv_out, int* tiny, void* k_scale,
-                                             int64_t at, bool store) {
+__device__ __forceinline__ void column_scale(float amax, float* pre, float* inv, int* tiny, void* k_scale, int64_t at,
+                                             bool store) {
     const GroupScale g = group_scale<E8M0>(amax);
-    *s_out = g.s;
-    *inv_out = g.inv;
-    if (g.s < kTinyScale) *tiny = 1;
+    *pre = g.pre;
+    *inv = g.inv;
+    if (g.pre != 1.f) *tiny = 1;
     if (store) {
         if (E8M0) ((uint8_t*)k_scale)[at] = (uint8_t)g.byte;
         else ((float*)k_scale)[at] = g.s;
@@ -242,106 +262,139 @@ __device__ __forceinline__ void column_scale(float amax, float* s_out, float* in
 }
 
 template <int N>
-__device__ __forceinline__ void quantize_columns(const float* v, const float* s, const float* inv, bool tiny,
+__device__ __forceinline__ void quantize_columns(const float* v, const float* pre, const float* inv, bool tiny,
                                                  uint32_t (&q)[N / 4]) {
+    if (!tiny) {
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-        if (tiny) {
-            q[i / 4] = e4m3_x4(tiny_quotient(v[i], s[i]), tiny_quotient(v[i + 1], s[i + 1]),
-                               tiny_quotient(v[i + 2], s[i + 2]), tiny_quotient(v[i + 3], s[i + 3]));
-        } else {
+        for (int i = 0; i < N; i += 4)
             q[i / 4] = e4m3_x4(v[i] * inv[i], v[i + 1] * inv[i + 1], v[i + 2] * inv[i + 2], v[i + 3] * inv[i + 3]);
-        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            q[i / 4] = e4m3_x4(tiny_quotient(v[i], pre[i], inv[i]), tiny_quotient(v[i + 1], pre[i + 1], inv[i + 1]),
+                               tiny_quotient(v[i + 2], pre[i + 2], inv[i + 2]),
+                               tiny_quotient(v[i + 3], pre[i + 3], inv[i + 3]));
     }
 }
 
 // ----------------------------------------------------------------- fp8 backward
 
-// A workgroup takes a token group x 256 gate/up columns: 8 waves, 32 rows at
-// a time, 4 times.  The gradients stay in registers in fp32 between the row
-// scales (DPP) and the column scales (registers, lane swaps, LDS), so that the
-// checkpoint and dH are read and SwiGLU is evaluated once.
-constexpr int kBwdThreads = 512, kBwdWaves = kBwdThreads / 64, kBwdPasses = 128 / (kBwdThreads / 16);
+// A workgroup takes a token group x 128 gate/up columns (8 lanes a row): 4
+// waves, 32 rows at a time, 4 times.  The gradients stay in registers in fp32
+// between the row scales (DPP) and the column scales (registers, lane swaps,
+// LDS), so that the checkpoint and dH are read and SwiGLU is evaluated once.
+// Rows past the group are out of their buffers' range: they read as 0 and
+// their stores are dropped.
+constexpr int kBwdCols = 128, kBwdRows = kThreads / 8, kBwdPasses = 128 / kBwdRows;
+constexpr int kBwdRun = 16;
+
+__device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t soff) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)off, (int)soff, CP_NT));
+}
 
 template <OperandFormat FMT, bool E8M0>
-__global__ __launch_bounds__(kBwdThreads, 2) void swiglu_backward_fp8_kernel(CheckpointArgs a) {
-    constexpr int C = kUnit + 128;                       // columns of dGU (in lane order), then of H
-    __shared__ float red_s[kBwdWaves][C];
-    __shared__ float s_s[C], inv_s[C];
+__global__ __launch_bounds__(kThreads) void swiglu_backward_fp8_kernel(CheckpointArgs a) {
+    constexpr int C = kBwdCols + kBwdCols / 2;           // columns of dGU (in lane order), then of H
+    __shared__ float red_s[kThreads / 64][C];
+    __shared__ float pre_s[C], inv_s[C];
     __shared__ int tiny_s;
-    const int upr = a.W / 128;
-    const int want = blockIdx.x / upr, unit = blockIdx.x % upr;
+    const int upr = a.W / 64;                            // units of a row
+    const int64_t tile = work_position<kBwdRun>();
+    const int want = (int)(tile / upr), unit = (int)(tile - (int64_t)want * upr);
     const TokenGroup tg = token_group(a.m_sizes, a.G, a.rows, want);
     if (tg.n <= 0) return;
-    const int lane = threadIdx.x & 63, l16 = lane & 15, wave = threadIdx.x >> 6;
-    const bool odd = l16 & 1;
+    const int lane = threadIdx.x & 63, l8 = lane & 7;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const bool odd = l8 & 1;
     if (threadIdx.x == 0) tiny_s = 0;
+    const int64_t u = (int64_t)tg.row * upr + unit;      // units before the tile's first
+    const uint32_t units = (uint32_t)tg.n * upr - unit;  // from there to the group's end
+    const int r0 = wave * 8 + (lane >> 3);
+    const uint32_t at = (uint32_t)(r0 * upr);
+    u32x4 codes[kBwdPasses], dh[kBwdPasses];
+    float scale[kBwdPasses];
+    {
+        auto ck = make_rsrc(a.ckpt + u * kBwdCols, units * kBwdCols);
+        auto in = make_rsrc((const uint16_t*)a.in + u * 64, units * 128);
+        auto sc = make_rsrc(a.ckpt_scale + u, units * 4);
+#pragma unroll
+        for (int p = 0; p < kBwdPasses; ++p) {
+            const uint32_t step = (uint32_t)(p * kBwdRows * upr);
+            codes[p] = buffer_load16(ck, at * kBwdCols + l8 * 16, step * kBwdCols);
+            dh[p] = buffer_load16(in, at * 128 + l8 * 16, step * 128);
+            scale[p] = __uint_as_float(
+                (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(sc, (int)(at * 4), (int)(step * 4), 0));
+        }
+    }
     float v[kBwdPasses][24];                             // 8 of gate, 8 of up, 8 of H
-    const int r0 = wave * 4 + (lane >> 4);
+    {
+        auto out = make_rsrc((const uint8_t*)a.row_out + u * kBwdCols, units * kBwdCols);
+        auto out_scale = FMT == kRows ? make_rsrc((const float*)a.row_scale + u, units * 4)
+                                      : make_rsrc((const float*)a.row_scale + (int64_t)unit * a.rows + tg.row, tg.n * 4);
+        const int scale_at = l8 ? -1 : (FMT == kRows ? (int)(at * 4) : r0 * 4);   // -1: out of range
+        const int scale_step = FMT == kRows ? upr * 4 : 4;
 #pragma unroll
-    for (int p = 0; p < kBwdPasses; ++p) {
-        const int r = r0 + p * (kBwdThreads / 16);
-        const bool in = r < tg.n;
-        const int64_t row = tg.row + r, u = row * upr + unit;
-        u32x4 codes = {0, 0, 0, 0}, dh = {0, 0, 0, 0};
-        float scale = 0.f;
-        if (in) {
-            codes = *(const u32x4*)(a.ckpt + u * kUnit + l16 * 16);
-            dh = *(const u32x4*)((const uint16_t*)a.in + u * 128 + l16 * 8);
-            scale = a.ckpt_scale[u * 2 + (l16 >> 3)];
-        }
-        swiglu_grad8(codes, scale, dh, odd, v[p], v[p] + 8, v[p] + 16);
-        const GroupScale g = group_scale<false>(max8(amax8(v[p] + 8, amax8(v[p], 0.f))));
-        const u32x4 q = join_codes(quantize8(v[p], g), quantize8(v[p] + 8, g), odd);
-        if (in) {
-            *(u32x4*)((uint8_t*)a.row_out + u * kUnit + l16 * 16) = q;
-            if ((l16 & 7) == 0) store_scale<FMT>(a.row_scale, row, unit * 2 + (l16 >> 3), upr * 2, a.rows, g.s);
+        for (int p = 0; p < kBwdPasses; ++p) {
+            swiglu_grad8(codes[p], scale[p], dh[p], odd, v[p], v[p] + 8, v[p] + 16);
+            const GroupScale g = group_scale<false>(max8(amax8(v[p] + 8, amax8(v[p], 0.f))));
+            uint32_t q[4];
+            quantize<16>(v[p], g, q);
+            __builtin_amdgcn_raw_buffer_store_b128(join_codes(u32x2{q[0], q[1]}, u32x2{q[2], q[3]}, odd), out,
+                                                   (int)(at * kBwdCols + l8 * 16), p * kBwdRows * upr * kBwdCols, CP_NT);
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(g.s), out_scale, scale_at, p * kBwdRows * scale_step, 0);
+            __builtin_amdgcn_sched_barrier(0);           // one pass's temporaries at a time
         }
     }
-    float m[24], red[6];
-#pragma unroll
-    for (int i = 0; i < 24; ++i) {
-        m[i] = 0.f;
-#pragma unroll
-        for (int p = 0; p < kBwdPasses; ++p) m[i] = fmaxf(m[i], fabsf(v[p][i]));
-    }
-    reduce_rows<24>(m, red);
     const int sub = lane >> 4, perm = sub == 1 ? 2 : (sub == 2 ? 1 : sub);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) red_s[wave][l16 * 16 + 4 * i + perm] = red[i];
+    for (int part = 0; part < 3; ++part) {               // gate, up, H: few registers beside v
+        float m[8], red[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) red_s[wave][kUnit + l16 * 8 + 4 * i + perm] = red[4 + i];
+        for (int i = 0; i < 8; ++i) {
+            float y = 0.f;
+#pragma unroll
+            for (int p = 0; p < kBwdPasses; ++p) y = fmaxf(y, fabsf(v[p][part * 8 + i]));
+            // the two rows of a 16-lane row
+            m[i] = __uint_as_float(max(__float_as_uint(y), lane_of<DPP_ROR8>(__float_as_uint(y))));
+        }
+        reduce_rows<8>(m, red);
+        float* to = red_s[wave] + (part < 2 ? l8 * 16 + part * 8 : kBwdCols + l8 * 8) + perm;
+        to[0] = red[0];                                  // the 16-lane row's halves hold the same
+        to[4] = red[1];
+        __builtin_amdgcn_sched_barrier(0);
+    }
     __syncthreads();
     if (threadIdx.x < C) {
         const int c = threadIdx.x;
-        float x = 0.f;
+        float y = 0.f;
 #pragma unroll
-        for (int w = 0; w < kBwdWaves; ++w) x = fmaxf(x, red_s[w][c]);
+        for (int w = 0; w < kThreads / 64; ++w) y = fmaxf(y, red_s[w][c]);
         const bool store = want < a.scale_groups;
-        if (c < kUnit) {
+        if (c < kBwdCols) {
             const int l = c >> 4, i = c & 15;            // lane l: 8 gate columns, then the 8 up columns 16 further on
             const int col = 32 * (l >> 1) + 8 * (l & 1) + (i < 8 ? i : i + 8);
-            column_scale<E8M0>(x, &s_s[c], &inv_s[c], &tiny_s, a.k_scale,
-                               (int64_t)want * (2 * a.W) + unit * kUnit + col, store);
+            column_scale<E8M0>(y, &pre_s[c], &inv_s[c], &tiny_s, a.k_scale,
+                               (int64_t)want * (2 * a.W) + unit * kBwdCols + col, store);
         } else {
-            column_scale<E8M0>(x, &s_s[c], &inv_s[c], &tiny_s, a.hk_scale, (int64_t)want * a.W + unit * 128 + c - kUnit,
-                               store);
+            column_scale<E8M0>(y, &pre_s[c], &inv_s[c], &tiny_s, a.hk_scale,
+                               (int64_t)want * a.W + unit * 64 + c - kBwdCols, store);
         }
     }
     __syncthreads();
     const bool tiny = tiny_s;
+    auto k_out = make_rsrc(a.k_out + u * kBwdCols, units * kBwdCols);
+    auto hk_out = make_rsrc(a.hk_out + u * 64, units * 64);
 #pragma unroll
     for (int p = 0; p < kBwdPasses; ++p) {
-        const int r = r0 + p * (kBwdThreads / 16);
-        const int64_t u = (int64_t)(tg.row + r) * upr + unit;
         uint32_t q[4], qh[2];
-        quantize_columns<16>(v[p], s_s + l16 * 16, inv_s + l16 * 16, tiny, q);
-        quantize_columns<8>(v[p] + 16, s_s + kUnit + l16 * 8, inv_s + kUnit + l16 * 8, tiny, qh);
-        const u32x4 c = join_codes(u32x2{q[0], q[1]}, u32x2{q[2], q[3]}, odd);
-        if (r < tg.n) {
-            *(u32x4*)(a.k_out + u * kUnit + l16 * 16) = c;
-            *(u32x2*)(a.hk_out + u * 128 + l16 * 8) = u32x2{qh[0], qh[1]};
-        }
+        asm volatile("" ::: "memory");                   // 24 inverses from LDS again, not in registers beside v
+        quantize_columns<16>(v[p], pre_s + l8 * 16, inv_s + l8 * 16, tiny, q);
+        quantize_columns<8>(v[p] + 16, pre_s + kBwdCols + l8 * 8, inv_s + kBwdCols + l8 * 8, tiny, qh);
+        const uint32_t step = (uint32_t)(p * kBwdRows * upr);
+        __builtin_amdgcn_raw_buffer_store_b128(join_codes(u32x2{q[0], q[1]}, u32x2{q[2], q[3]}, odd), k_out,
+                                               (int)(at * kBwdCols + l8 * 16), (int)(step * kBwdCols), CP_NT);
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{qh[0], qh[1]}, hk_out, (int)(at * 64 + l8 * 8), (int)(step * 64),
+                                              CP_NT);
     }
 }
 
@@ -350,38 +403,46 @@ __global__ __launch_bounds__(kBwdThreads, 2) void swiglu_backward_fp8_kernel(Che
 // A workgroup takes a token group x 256 columns: 4 waves, 16 rows at a time, 8
 // times.  The codes (or bf16 values) stay in registers as they were read, and
 // are scaled twice: for the columns' maxima and for the new codes.
-constexpr int kKgPasses = 128 / (kThreads / 16);
+constexpr int kKgRows = kThreads / 16, kKgPasses = 128 / kKgRows, kKgRun = 8;
 
 template <OperandFormat FMT, bool E8M0>
 __global__ __launch_bounds__(kThreads) void k_groups_kernel(CheckpointArgs a) {
     __shared__ float red_s[kThreads / 64][kUnit];
-    __shared__ float s_s[kUnit], inv_s[kUnit];
+    __shared__ float pre_s[kUnit], inv_s[kUnit];
     __shared__ int tiny_s;
     constexpr int RAW = FMT == kBf16 ? 2 : 1;
-    const int upr = a.W / kUnit, groups = a.W / kGroup;
-    const int want = blockIdx.x / upr, unit = blockIdx.x % upr;
+    const int upr = a.W / kUnit;                         // units of a row
+    const int64_t tile = work_position<kKgRun>();
+    const int want = (int)(tile / upr), unit = (int)(tile - (int64_t)want * upr);
     const TokenGroup tg = token_group(a.m_sizes, a.G, a.rows, want);
     if (tg.n <= 0) return;
-    const int lane = threadIdx.x & 63, l16 = lane & 15, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, l16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     if (threadIdx.x == 0) tiny_s = 0;
-    const int r0 = wave * 4 + (lane >> 4), kg = unit * 2 + (l16 >> 3);
+    const int64_t u = (int64_t)tg.row * upr + unit;      // units before the tile's first
+    const uint32_t units = (uint32_t)tg.n * upr - unit;  // from there to the group's end
+    const int r0 = wave * 4 + (lane >> 4);
+    const uint32_t at = (uint32_t)(r0 * upr);
     u32x4 raw[kKgPasses][RAW];
     float scale[kKgPasses];
+    {
+        auto in = make_rsrc((const uint8_t*)a.in + u * kUnit * RAW, units * kUnit * RAW);
+        auto sc = make_rsrc(FMT == kRows ? a.in_scale + u * 2 : nullptr, units * 8);
+        const int half = l16 >> 3;                       // the row's 128-column half
 #pragma unroll
-    for (int p = 0; p < kKgPasses; ++p) {
-        const int r = r0 + p * (kThreads / 16);
-        const int64_t row = tg.row + r;
+        for (int p = 0; p < kKgPasses; ++p) {
+            const uint32_t step = (uint32_t)(p * kKgRows);
 #pragma unroll
-        for (int i = 0; i < RAW; ++i) raw[p][i] = u32x4{0, 0, 0, 0};
-        scale[p] = 0.f;
-        if (r < tg.n) {
-            if (FMT == kBf16) {
-                const u32x4* q = (const u32x4*)((const uint16_t*)a.in + row * a.W + unit * kUnit + l16 * 16);
-                raw[p][0] = q[0];
-                raw[p][RAW - 1] = q[1];
-            } else {
-                raw[p][0] = *(const u32x4*)((const uint8_t*)a.in + row * a.W + unit * kUnit + l16 * 16);
-                scale[p] = FMT == kRows ? a.in_scale[row * groups + kg] : a.in_scale[(int64_t)kg * a.rows + row];
+            for (int i = 0; i < RAW; ++i)
+                raw[p][i] = buffer_load16(in, (at * kUnit + l16 * 16) * RAW + i * 16, step * upr * kUnit * RAW);
+            scale[p] = 0.f;
+            if (FMT == kRows)
+                scale[p] = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+                    sc, (int)(at * 8 + half * 4), (int)(step * upr * 8), 0));
+            if (FMT == kKm) {
+                const int r = r0 + (int)step;            // rows of other groups follow: not out of range
+                const float x = a.in_scale[(int64_t)(unit * 2 + half) * a.rows + min(tg.row + r, a.rows - 1)];
+                scale[p] = r < tg.n ? x : 0.f;
             }
         }
     }
@@ -404,7 +465,10 @@ __global__ __launch_bounds__(kThreads) void k_groups_kernel(CheckpointArgs a) {
         float v[16];
         values(p, v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) m[i] = fmaxf(m[i], fabsf(v[i]));
+        for (int i = 0; i < 16; ++i) {
+            m[i] = fmaxf(m[i], fabsf(v[i]));
+            asm volatile("" : "+v"(m[i]));               // now, not when all values are there
+        }
     }
     reduce_rows<16>(m, red);
     const int sub = lane >> 4, perm = sub == 1 ? 2 : (sub == 2 ? 1 : sub);
@@ -416,29 +480,29 @@ __global__ __launch_bounds__(kThreads) void k_groups_kernel(CheckpointArgs a) {
         float x = 0.f;
 #pragma unroll
         for (int w = 0; w < kThreads / 64; ++w) x = fmaxf(x, red_s[w][c]);
-        column_scale<E8M0>(x, &s_s[c], &inv_s[c], &tiny_s, a.k_scale, (int64_t)want * a.W + unit * kUnit + c,
+        column_scale<E8M0>(x, &pre_s[c], &inv_s[c], &tiny_s, a.k_scale, (int64_t)want * a.W + unit * kUnit + c,
                            want < a.scale_groups);
     }
     __syncthreads();
     const bool tiny = tiny_s;
+    auto k_out = make_rsrc(a.k_out + u * kUnit, units * kUnit);
 #pragma unroll
     for (int p = 0; p < kKgPasses; ++p) {
-        const int r = r0 + p * (kThreads / 16);
         float v[16];
         uint32_t q[4];
+#pragma unroll
+        for (int i = 0; i < RAW; ++i) asm volatile("" : "+v"(raw[p][i]));   // scaled anew, not kept in fp32
         values(p, v);
-        quantize_columns<16>(v, s_s + l16 * 16, inv_s + l16 * 16, tiny, q);
-        if (r < tg.n)
-            *(u32x4*)(a.k_out + (int64_t)(tg.row + r) * a.W + unit * kUnit + l16 * 16) = u32x4{q[0], q[1], q[2], q[3]};
+        quantize_columns<16>(v, pre_s + l16 * 16, inv_s + l16 * 16, tiny, q);
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4{q[0], q[1], q[2], q[3]}, k_out, (int)(at * kUnit + l16 * 16),
+                                               (int)(p * kKgRows * upr * kUnit), CP_NT);
     }
 }
 
 // ----------------------------------------------------------------- launches
 
-// Workgroups of the row-wise kernels: 8 a CU, fewer where there are not that many units.
 static dim3 row_grid(const CheckpointArgs& a) {
-    const int64_t units = (int64_t)a.rows * (a.W / 128), blocks = (units + 15) / 16;
-    return dim3((unsigned)(blocks >= 2048 ? 2048 : (blocks + kXcds - 1) / kXcds * kXcds));
+    return run_grid<kRowRun>(((int64_t)a.rows * (a.W / 128) + 15) / 16);
 }
 
 // Token groups of any histogram: each expert can leave one short group.
@@ -463,13 +527,13 @@ hipError_t launch_swiglu_checkpoint_backward(const CheckpointArgs& a, hipStream_
 
 hipError_t launch_swiglu_checkpoint_backward_fp8(const CheckpointArgs& a, hipStream_t s) {
     if (a.rows == 0) return hipSuccess;
-    const dim3 grid((unsigned)(most_groups(a) * (a.W / 128)));
+    const dim3 grid = run_grid<kBwdRun>(most_groups(a) * (a.W / 64));
     if (a.fmt == kRows) {
-        if (a.k_e8m0) swiglu_backward_fp8_kernel<kRows, true><<<grid, kBwdThreads, 0, s>>>(a);
-        else swiglu_backward_fp8_kernel<kRows, false><<<grid, kBwdThreads, 0, s>>>(a);
+        if (a.k_e8m0) swiglu_backward_fp8_kernel<kRows, true><<<grid, kThreads, 0, s>>>(a);
+        else swiglu_backward_fp8_kernel<kRows, false><<<grid, kThreads, 0, s>>>(a);
     } else {
-        if (a.k_e8m0) swiglu_backward_fp8_kernel<kKm, true><<<grid, kBwdThreads, 0, s>>>(a);
-        else swiglu_backward_fp8_kernel<kKm, false><<<grid, kBwdThreads, 0, s>>>(a);
+        if (a.k_e8m0) swiglu_backward_fp8_kernel<kKm, true><<<grid, kThreads, 0, s>>>(a);
+        else swiglu_backward_fp8_kernel<kKm, false><<<grid, kThreads, 0, s>>>(a);
     }
     return hipGetLastError();
 }
@@ -482,7 +546,7 @@ static void k_groups_as(const CheckpointArgs& a, dim3 grid, hipStream_t s) {
 
 hipError_t launch_checkpoint_to_k_groups(const CheckpointArgs& a, hipStream_t s) {
     if (a.rows == 0) return hipSuccess;
-    const dim3 grid((unsigned)(most_groups(a) * (a.W / kUnit)));
+    const dim3 grid = run_grid<kKgRun>(most_groups(a) * (a.W / kUnit));
     if (a.fmt == kBf16) k_groups_as<kBf16>(a, grid, s);
     else if (a.fmt == kRows) k_groups_as<kRows>(a, grid, s);
     else k_groups_as<kKm>(a, grid, s);

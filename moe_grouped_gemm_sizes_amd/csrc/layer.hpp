@@ -95,6 +95,25 @@ inline int route_tile_tokens(int T) {
 
 #ifdef __HIPCC__
 
+// ----------------------------------------------------------------- order of work
+
+constexpr int kXcds = 8;
+
+// Position of this workgroup's work: consecutive workgroups go to the 8 XCDs in
+// turn, and RUN neighbouring pieces of work to one XCD, so that all of the chip
+// works on one stretch of memory at a time and lines that neighbours share meet
+// in one L2.  The grid is a multiple of 8 RUN.
+template <int RUN>
+__device__ __forceinline__ int64_t work_position() {
+    const int order = blockIdx.x / kXcds;
+    return ((int64_t)(order / RUN) * kXcds + blockIdx.x % kXcds) * RUN + order % RUN;
+}
+template <int RUN>
+static dim3 run_grid(int64_t pieces) {
+    constexpr int64_t round = kXcds * RUN;
+    return dim3((unsigned)((pieces + round - 1) / round * round));
+}
+
 // ----------------------------------------------------------------- cross-lane
 
 // Lane exchange by DPP: CTRL is quad_perm, row_shr, row_ror, row_bcast, ...
@@ -111,18 +130,27 @@ constexpr int DPP_XOR1 = 0xB1;            // quad_perm [1,0,3,2]
 constexpr int DPP_XOR2 = 0x4E;            // quad_perm [2,3,0,1]
 constexpr int DPP_HALF_MIRROR = 0x141;    // lane i of 8 <-> 7 - i
 constexpr int DPP_MIRROR = 0x140;         // lane i of 16 <-> 15 - i
+constexpr int DPP_ROR4 = 0x124, DPP_ROR8 = 0x128;   // lane i of 16 <- i - 4, i - 8 mod 16
 constexpr int DPP_SHR = 0x110;            // + n: row_shr by n
 constexpr int DPP_BCAST15 = 0x142, DPP_BCAST31 = 0x143;
 
-// Maximum over each aligned group of 8 or 16 lanes, in every lane of it.
-__device__ __forceinline__ float max8(float v) {
-    v = fmaxf(v, dpp_f<DPP_XOR1>(v, v));
-    v = fmaxf(v, dpp_f<DPP_XOR2>(v, v));
-    return fmaxf(v, dpp_f<DPP_HALF_MIRROR>(v, v));
+// Lane exchange in which every lane has a source.
+template <int CTRL>
+__device__ __forceinline__ uint32_t lane_of(uint32_t x) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xF, 0xF, true);
 }
-__device__ __forceinline__ float max16(float v) {
-    v = max8(v);
-    return fmaxf(v, dpp_f<DPP_MIRROR>(v, v));
+// Maximum over each aligned group of 8 or 16 lanes, in every lane of it, of
+// floats that are not negative and not NaN: their bits compare as integers,
+// which needs no NaN handling and folds the lane exchange into the maximum.
+__device__ __forceinline__ float max8(float f) {
+    uint32_t v = __float_as_uint(f);
+    v = max(v, lane_of<DPP_XOR1>(v));
+    v = max(v, lane_of<DPP_XOR2>(v));
+    return __uint_as_float(max(v, lane_of<DPP_HALF_MIRROR>(v)));
+}
+__device__ __forceinline__ float max16(float f) {
+    const uint32_t v = __float_as_uint(max8(f));
+    return __uint_as_float(max(v, lane_of<DPP_MIRROR>(v)));
 }
 
 // Wave-wide reductions: an inclusive scan by DPP whose last lane holds the
@@ -158,6 +186,19 @@ __device__ __forceinline__ float wave_sum(float v) {
     return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 
+// ----------------------------------------------------------------- streams
+
+// Accesses to data that this kernel does not touch again: marked so that
+// caches let go of them first.
+template <typename T>
+__device__ __forceinline__ T load_once(const T* p) {
+    return __builtin_nontemporal_load(p);
+}
+template <typename T>
+__device__ __forceinline__ void store_once(void* p, T v) {
+    __builtin_nontemporal_store(v, (T*)p);
+}
+
 // ----------------------------------------------------------------- numbers
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -191,18 +232,27 @@ __device__ __forceinline__ void e4m3_to_f32(uint32_t v, float* f) {
 }
 
 // One group's scale amax / 448 (1 where that is 0; POW2: the smallest power of
-// two that is at least it, from 2^-126 up, as value and E8M0 byte) and inv,
-// what values are multiplied with to become codes.  x * (1 / s) is within 1.5
-// ulp of x / s: it moves a code only where x / s is that near a rounding border.
+// two that is at least it, from 2^-126 up, as value and E8M0 byte) and pre and
+// inv, what values are multiplied with to become codes; pre is 1 but for scales
+// whose reciprocal may overflow.  With the hardware's reciprocal
+// (1 ulp) x * (1 / s) is within 2 ulp of x / s: it moves a code only where x / s is
+// that near a rounding border.
 struct GroupScale {
-    float s, inv;
+    float s, pre, inv;
     uint32_t byte;
 };
+constexpr float kTinyScale = 0x1p-100f;
 template <bool POW2>
 __device__ __forceinline__ GroupScale group_scale(float amax) {
     GroupScale g;
-    g.s = amax / 448.f;
-    if (!(g.s > 0.f)) g.s = 1.f;
+    // amax / 448 correctly rounded: the product with the rounded reciprocal, and its remainder
+    const float q = amax * (1.f / 448.f);
+    g.s = __builtin_fmaf(__builtin_fmaf(-448.f, q, amax), 1.f / 448.f, q);
+    if (!(g.s >= kTinyScale)) {                          // 0, tiny, or NaN of an infinite amax
+        g.s = amax / 448.f;
+        if (!(g.s > 0.f)) g.s = 1.f;
+    }
+    g.pre = 1.f;
     g.byte = 0;
     if (POW2) {
         const uint32_t b = __float_as_uint(g.s);
@@ -211,24 +261,32 @@ __device__ __forceinline__ GroupScale group_scale(float amax) {
         g.s = __uint_as_float(e << 23);
         g.inv = e == 255u ? 0.f : __uint_as_float((254u - e) << 23);
     } else {
-        g.inv = 1.f / g.s;
+        if (g.s < kTinyScale) g.pre = 0x1p+100f;
+        g.inv = __builtin_amdgcn_rcpf(g.s * g.pre);
     }
     return g;
 }
 
-// Code of one value whose group's scale s is so small that 1 / s may overflow
-// and s itself be rounded coarsely: a division, and the clamp that this needs.
-__device__ __forceinline__ float tiny_quotient(float x, float s) {
-    const float q = x / s;
+// Quotient where pre is not 1: a scale down there may itself be rounded so
+// coarsely (subnormals) that its largest value is past 448 times it.
+__device__ __forceinline__ float tiny_quotient(float x, float pre, float inv) {
+    const float q = x * pre * inv;
     return q != q ? q : fminf(fmaxf(q, -448.f), 448.f);
 }
-constexpr float kTinyScale = 0x1p-100f;
 
-// Four values of one group -> their codes.
-__device__ __forceinline__ uint32_t quantize_x4(float a, float b, float c, float d, const GroupScale& g) {
-    if (g.s < kTinyScale)
-        return e4m3_x4(tiny_quotient(a, g.s), tiny_quotient(b, g.s), tiny_quotient(c, g.s), tiny_quotient(d, g.s));
-    return e4m3_x4(a * g.inv, b * g.inv, c * g.inv, d * g.inv);
+// N values of one group -> their codes, four to a word.
+template <int N>
+__device__ __forceinline__ void quantize(const float* v, const GroupScale& g, uint32_t* q) {
+    if (g.pre == 1.f) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            q[i / 4] = e4m3_x4(v[i] * g.inv, v[i + 1] * g.inv, v[i + 2] * g.inv, v[i + 3] * g.inv);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            q[i / 4] = e4m3_x4(tiny_quotient(v[i], g.pre, g.inv), tiny_quotient(v[i + 1], g.pre, g.inv),
+                               tiny_quotient(v[i + 2], g.pre, g.inv), tiny_quotient(v[i + 3], g.pre, g.inv));
+    }
 }
 
 #endif  // __HIPCC__

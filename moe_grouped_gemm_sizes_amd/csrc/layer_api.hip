@@ -62,9 +62,8 @@ moegg_status_t check_permute(const int32_t* row_of, int T, int k, int W, int64_t
     if (!aligned(row_of, 4)) return MOEGG_ERR_INVALID_ARG;
     if (k > kRouteMaxTopK) return MOEGG_ERR_UNSUPPORTED;
     if ((int64_t)T * k > INT32_MAX) return MOEGG_ERR_UNSUPPORTED;
-    // one wave per token and 512 columns, or 256 lanes per token, rounded up to whole workgroups on every XCD
-    if (((int64_t)T * (((int64_t)W + 511) / 512) + 32) * 64 > kMaxWorkItems || ((int64_t)T + 4096) * 256 > kMaxWorkItems)
-        return MOEGG_ERR_UNSUPPORTED;
+    // a wave for each token and 512 columns, and up to 256 workgroups of 4 more
+    if (((int64_t)T * (((int64_t)W + 511) / 512) + 1024) * 64 > kMaxWorkItems) return MOEGG_ERR_UNSUPPORTED;
     return MOEGG_OK;
 }
 
@@ -82,7 +81,8 @@ moegg_status_t check_checkpoint(const int32_t* m_sizes, int G, int64_t rows, int
     if (!m_sizes || !aligned(m_sizes, 4) || G < 1 || G > kMaxExperts || rows < 0 || rows > INT32_MAX || W < 1)
         return MOEGG_ERR_INVALID_ARG;
     if (W % unit != 0) return MOEGG_ERR_UNSUPPORTED;
-    if ((rows / 128 + G) * (W / unit) * threads > kMaxWorkItems) return MOEGG_ERR_UNSUPPORTED;
+    // 128 rows of 4 W bytes are one buffer resource; the grid is rounded up by at most 1024 workgroups
+    if (W > 1 << 21 || ((rows / 128 + G) * (W / unit) + 1024) * threads > kMaxWorkItems) return MOEGG_ERR_UNSUPPORTED;
     return MOEGG_OK;
 }
 

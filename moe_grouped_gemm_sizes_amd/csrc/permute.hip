@@ -14,26 +14,20 @@
 namespace moegg {
 
 constexpr int kThreads = 256;
-constexpr int kXcds = 8;
 
-// Work item of a wave: consecutive workgroups go to the 8 XCDs in turn; giving
-// XCD x the x-th eighth of the items keeps the scales of neighbouring tokens,
-// which share cache lines when stored [groups, rows], in one L2.
-__device__ __forceinline__ int64_t wave_item(int64_t blocks_per_xcd) {
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    return ((int64_t)(blockIdx.x % kXcds) * blocks_per_xcd + blockIdx.x / kXcds) * (kThreads / 64) + wave;
+// Work item of a wave.
+constexpr int kItemRun = 32;              // neighbouring workgroups on one XCD
+__device__ __forceinline__ int64_t wave_item() {
+    return work_position<kItemRun>() * (kThreads / 64) + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
 }
-inline int64_t blocks_per_xcd(int64_t items) {
-    const int64_t blocks = (items + kThreads / 64 - 1) / (kThreads / 64);
-    return (blocks + kXcds - 1) / kXcds;
-}
+static dim3 item_grid(int64_t items) { return run_grid<kItemRun>((items + kThreads / 64 - 1) / (kThreads / 64)); }
 
 // Rows outside [0, rows) (no expert, over the capacity) are skipped.
 __device__ __forceinline__ int uniform_row(const int32_t* p) { return __builtin_amdgcn_readfirstlane(*p); }
 
 // Up to 8 bf16 of a row piece: one 16-byte load where all 8 are there.
 __device__ __forceinline__ u32x4 load8(const uint16_t* p, int n) {
-    if (n >= 8) return *(const u32x4_a2*)p;
+    if (n >= 8) return __builtin_nontemporal_load((const u32x4_a2*)p);
     uint32_t v[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 7; ++i)
@@ -42,7 +36,7 @@ __device__ __forceinline__ u32x4 load8(const uint16_t* p, int n) {
 }
 __device__ __forceinline__ void store8(uint16_t* p, u32x4 v, int n) {
     if (n >= 8) {
-        *(u32x4_a2*)p = v;
+        __builtin_nontemporal_store(v, (u32x4_a2*)p);
         return;
     }
 #pragma unroll
@@ -60,8 +54,8 @@ __device__ __forceinline__ void unpack8(u32x4 v, float* f) {
 // ----------------------------------------------------------------- dispatch
 
 // bf16: a wave copies 512 elements of a token to its k rows.
-__global__ __launch_bounds__(kThreads) void dispatch_bf16_kernel(PermuteArgs a, int64_t per_xcd, int chunks) {
-    const int64_t item = wave_item(per_xcd);
+__global__ __launch_bounds__(kThreads) void dispatch_bf16_kernel(PermuteArgs a, int chunks) {
+    const int64_t item = wave_item();
     if (item >= (int64_t)a.T * chunks) return;
     const int lane = threadIdx.x & 63;
     const int64_t t = item / chunks;
@@ -77,8 +71,8 @@ __global__ __launch_bounds__(kThreads) void dispatch_bf16_kernel(PermuteArgs a, 
 // e4m3: a wave quantizes 1024 elements (8 groups) of a token, 16 a lane, and
 // stores them to its k rows.
 template <OperandFormat FMT>
-__global__ __launch_bounds__(kThreads) void dispatch_fp8_kernel(PermuteArgs a, int64_t per_xcd, int chunks) {
-    const int64_t item = wave_item(per_xcd);
+__global__ __launch_bounds__(kThreads) void dispatch_fp8_kernel(PermuteArgs a, int chunks) {
+    const int64_t item = wave_item();
     if (item >= (int64_t)a.T * chunks) return;
     const int lane = threadIdx.x & 63;
     const int64_t t = item / chunks;
@@ -87,8 +81,8 @@ __global__ __launch_bounds__(kThreads) void dispatch_fp8_kernel(PermuteArgs a, i
     u32x4 x0 = {0, 0, 0, 0}, x1 = {0, 0, 0, 0};
     if (in) {
         const u32x4* p = (const u32x4*)((const uint16_t*)a.x + t * a.W + c);
-        x0 = p[0];
-        x1 = p[1];
+        x0 = load_once(p);
+        x1 = load_once(p + 1);
     }
     float f[16];
     unpack8(x0, f);
@@ -97,9 +91,9 @@ __global__ __launch_bounds__(kThreads) void dispatch_fp8_kernel(PermuteArgs a, i
 #pragma unroll
     for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(f[i]));
     const GroupScale g = group_scale<FMT == kE8m0>(max8(m));
-    u32x4 q;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = quantize_x4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3], g);
+    uint32_t codes[4];
+    quantize<16>(f, g, codes);
+    const u32x4 q = {codes[0], codes[1], codes[2], codes[3]};
     const int kg = c / kGroup, groups = a.W / kGroup;
     for (int j0 = 0; j0 < a.k; j0 += 8) {
         // a group's 8 lanes store its scale to 8 rows
@@ -113,7 +107,8 @@ __global__ __launch_bounds__(kThreads) void dispatch_fp8_kernel(PermuteArgs a, i
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int row = __builtin_amdgcn_readlane(srow, j);
-            if (in && (uint32_t)row < (uint32_t)a.rows) *(u32x4*)((uint8_t*)a.out + (int64_t)row * a.W + c) = q;
+            if (in && (uint32_t)row < (uint32_t)a.rows) 
+                store_once((uint8_t*)a.out + (int64_t)row * a.W + c, q);
         }
     }
 }
@@ -122,8 +117,8 @@ __global__ __launch_bounds__(kThreads) void dispatch_fp8_kernel(PermuteArgs a, i
 
 // A wave sums 512 columns of a token's rows in fp32, in the order of its
 // assignments, and rounds once.  Eight rows are in flight at a time.
-__global__ __launch_bounds__(kThreads) void combine_kernel(PermuteArgs a, int64_t per_xcd, int chunks) {
-    const int64_t item = wave_item(per_xcd);
+__global__ __launch_bounds__(kThreads) void combine_kernel(PermuteArgs a, int chunks) {
+    const int64_t item = wave_item();
     if (item >= (int64_t)a.T * chunks) return;
     const int lane = threadIdx.x & 63;
     const int64_t t = item / chunks;
@@ -216,11 +211,11 @@ __global__ __launch_bounds__(1024) void combine_backward_kernel(PermuteArgs a) {
                 } else {
                     // rounding keeps order: the largest |w d| is |w| times the largest |d|, rounded
                     const GroupScale g = group_scale<FMT == kE8m0>(fabsf(w * amax));
-                    u32x2 q;
-                    q.x = quantize_x4(o[0], o[1], o[2], o[3], g);
-                    q.y = quantize_x4(o[4], o[5], o[6], o[7], g);
+                    uint32_t codes[2];
+                    quantize<8>(o, g, codes);
+                    const u32x2 q = {codes[0], codes[1]};
                     if (n > 0) {
-                        *(u32x2*)((uint8_t*)a.out + (int64_t)row * a.W + c) = q;
+                        store_once((uint8_t*)a.out + (int64_t)row * a.W + c, q);
                         if ((lane & 15) == 0) {
                             const int kg = c / kGroup;
                             if (FMT == kRows) ((float*)a.scale)[(int64_t)row * groups + kg] = g.s;
@@ -251,13 +246,12 @@ __global__ __launch_bounds__(1024) void combine_backward_kernel(PermuteArgs a) {
 hipError_t launch_dispatch(const PermuteArgs& a, hipStream_t s) {
     if (a.T == 0) return hipSuccess;
     const int chunks = a.fmt == kBf16 ? (a.W + 511) / 512 : (a.W + 1023) / 1024;
-    const int64_t per_xcd = blocks_per_xcd((int64_t)a.T * chunks);
-    const dim3 grid((unsigned)(per_xcd * kXcds));
+    const dim3 grid = item_grid((int64_t)a.T * chunks);
     switch (a.fmt) {
-        case kBf16: dispatch_bf16_kernel<<<grid, kThreads, 0, s>>>(a, per_xcd, chunks); break;
-        case kRows: dispatch_fp8_kernel<kRows><<<grid, kThreads, 0, s>>>(a, per_xcd, chunks); break;
-        case kKm: dispatch_fp8_kernel<kKm><<<grid, kThreads, 0, s>>>(a, per_xcd, chunks); break;
-        case kE8m0: dispatch_fp8_kernel<kE8m0><<<grid, kThreads, 0, s>>>(a, per_xcd, chunks); break;
+        case kBf16: dispatch_bf16_kernel<<<grid, kThreads, 0, s>>>(a, chunks); break;
+        case kRows: dispatch_fp8_kernel<kRows><<<grid, kThreads, 0, s>>>(a, chunks); break;
+        case kKm: dispatch_fp8_kernel<kKm><<<grid, kThreads, 0, s>>>(a, chunks); break;
+        case kE8m0: dispatch_fp8_kernel<kE8m0><<<grid, kThreads, 0, s>>>(a, chunks); break;
     }
     return hipGetLastError();
 }
@@ -265,16 +259,14 @@ hipError_t launch_dispatch(const PermuteArgs& a, hipStream_t s) {
 hipError_t launch_combine(const PermuteArgs& a, hipStream_t s) {
     if (a.T == 0) return hipSuccess;
     const int chunks = (a.W + 511) / 512;
-    const int64_t per_xcd = blocks_per_xcd((int64_t)a.T * chunks);
-    combine_kernel<<<dim3((unsigned)(per_xcd * kXcds)), kThreads, 0, s>>>(a, per_xcd, chunks);
+    combine_kernel<<<item_grid((int64_t)a.T * chunks), kThreads, 0, s>>>(a, chunks);
     return hipGetLastError();
 }
 
 hipError_t launch_combine_backward(const PermuteArgs& a, hipStream_t s) {
     if (a.T == 0) return hipSuccess;
-    // few tokens: more waves on each, as far as its width gives them work
-    int threads = 256;
-    while (threads < 1024 && (int64_t)a.T * threads < 256 * 1024 && threads * 8 < a.W) threads *= 2;
+    // a wave for each 512 columns, up to 16: 14 waves on 7168 columns take 189 us where 4 take 202
+    const int threads = 64 * (a.W >= 16 * 512 ? 16 : (a.W + 511) / 512);
     switch (a.fmt) {
         case kBf16: combine_backward_kernel<kBf16><<<a.T, threads, 0, s>>>(a); break;
         case kRows: combine_backward_kernel<kRows><<<a.T, threads, 0, s>>>(a); break;
