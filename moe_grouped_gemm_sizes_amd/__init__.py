@@ -166,12 +166,14 @@ def _p(t: Optional[torch.Tensor]):
         raise ValueError("device tensor expected")
     if not t.is_contiguous():
         raise ValueError("contiguous tensor expected")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    # the handle alone: torch.cuda.current_stream() builds a Stream object, 2.8 us of a call's 10
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _check(status: int, what: str):
@@ -187,6 +189,8 @@ def _need(t: Optional[torch.Tensor], name: str, shape: Sequence[Optional[int]], 
     The library sees only pointers, so every extent it will index is checked here."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: tensor expected")
+    if t.dtype in dtypes and t.shape == tuple(shape):
+        return
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
     if t.dim() != len(shape) or any(x is not None and d != x for d, x in zip(t.shape, shape)):
@@ -200,9 +204,14 @@ def _none(t, name: str, why: str):
 
 
 def _one_device(*ts):
-    devs = {t.device for t in ts if isinstance(t, torch.Tensor)}
-    if len(devs) > 1:
-        raise ValueError(f"tensors on several devices: {sorted(str(d) for d in devs)}")
+    first = None
+    for t in ts:
+        if isinstance(t, torch.Tensor):
+            if first is None:
+                first = t.get_device()
+            elif t.get_device() != first:
+                devs = {t.device for t in ts if isinstance(t, torch.Tensor)}
+                raise ValueError(f"tensors on several devices: {sorted(str(d) for d in devs)}")
 
 
 def _ws(ws, G: int, max_rows: int):
@@ -583,9 +592,24 @@ def route_workspace(T: int, E: int, device="cuda") -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+def _top_k(t, name: str, T: int) -> int:
+    """k of an int32 [T, k] tensor."""
+    if isinstance(t, torch.Tensor) and t.dim() == 2:
+        k = t.shape[1]
+        _need(t, name, (T, k), (torch.int32,))
+        return k
+    _need(t, name, (T, None), (torch.int32,))
+
+
+def _matrix(t, name: str, dtypes):
+    """Shape of a matrix of one of `dtypes`."""
+    if not (isinstance(t, torch.Tensor) and t.dim() == 2 and t.dtype in dtypes):
+        _need(t, name, (None, None), dtypes)
+    return t.shape
+
+
 def _logits(logits) -> Tuple[int, int, int]:
-    _need(logits, "logits", [None, None], (torch.float32, torch.bfloat16))
-    T, E = logits.shape
+    T, E = _matrix(logits, "logits", (torch.float32, torch.bfloat16))
     return T, E, LOGITS_BF16 if logits.dtype == torch.bfloat16 else LOGITS_FP32
 
 
@@ -597,8 +621,7 @@ def route(logits, ids, weights, m_sizes, row_of, ws, *, rows_total: int, bias=No
     assignment in the contiguous layout of rows_total rows, or with cap > 0 in [E, cap] capacity buffers
     (rows_total = E * cap); -1 where there is none.  ws: route_workspace(T, E)."""
     T, E, kind = _logits(logits)
-    _need(ids, "ids", [T, None], (torch.int32,))
-    k = ids.shape[1]
+    k = _top_k(ids, "ids", T)
     _need(weights, "weights", [T, k], (torch.float32,))
     _need(m_sizes, "m_sizes", [E], (torch.int32,))
     _need(row_of, "row_of", [T, k], (torch.int32,))
@@ -618,8 +641,7 @@ def route_backward(logits, ids, d_weights, d_logits, *, score: int = SCORE_SOFTM
                    scale: float = 1.0, stream=None):
     """d_logits [T, E] (logits' dtype) from d_weights [T, k] and the ids that route chose (see moegg.h)."""
     T, E, kind = _logits(logits)
-    _need(ids, "ids", [T, None], (torch.int32,))
-    k = ids.shape[1]
+    k = _top_k(ids, "ids", T)
     _need(d_weights, "d_weights", [T, k], (torch.float32,))
     _need(d_logits, "d_logits", [T, E], (logits.dtype,))
     _one_device(logits, ids, d_weights, d_logits)
@@ -631,7 +653,7 @@ def _row_operand(A, name: str, A_scale, width: int, scale_km: bool) -> Tuple[int
     """Rows and operand type code of an expert-side operand [rows, width] or [G, cap, width] and its scales."""
     if not isinstance(A, torch.Tensor) or A.dim() not in (2, 3):
         raise ValueError(f"{name}: tensor [rows, width] or [G, cap, width] expected")
-    _need(A, name, [None] * (A.dim() - 1) + [width], (torch.bfloat16, _E4M3))
+    _need(A, name, (*A.shape[:-1], width), (torch.bfloat16, _E4M3))
     rows = A.shape[0] if A.dim() == 2 else A.shape[0] * A.shape[1]
     if A.dtype == torch.bfloat16:
         _none(A_scale, f"{name}_scale", "for a bf16 operand")
@@ -654,50 +676,47 @@ def dispatch(x, row_of, A, A_scale=None, *, scale_km: bool = False, stream=None)
     """A[row_of[t, j]] = x[t] (see moegg.h).  x bf16 [T, K]; A bf16 or e4m3, [rows, K] or [G, cap, K], with the
     scales of the grouped GEMM that reads it: fp32 [rows, K/128] ([G, cap, K/128]), [K/128, rows] (scale_km), or
     uint8 E8M0 bytes [K/128, rows]."""
-    _need(x, "x", [None, None], (torch.bfloat16,))
-    T, K = x.shape
-    _need(row_of, "row_of", [T, None], (torch.int32,))
+    T, K = _matrix(x, "x", (torch.bfloat16,))
+    k = _top_k(row_of, "row_of", T)
     rows, code = _row_operand(A, "A", A_scale, K, scale_km)
     _one_device(x, row_of, A, A_scale)
-    _check(lib().moegg_dispatch(_p(x), _p(row_of), _p(A), _p(A_scale), T, row_of.shape[1], K, rows, code,
+    _check(lib().moegg_dispatch(_p(x), _p(row_of), _p(A), _p(A_scale), T, k, K, rows, code,
                                 _stream(stream)), "moegg_dispatch")
 
 
 def _expert_rows(Y, N: int) -> int:
     if not isinstance(Y, torch.Tensor) or Y.dim() not in (2, 3):
         raise ValueError("Y: tensor [rows, N] or [G, cap, N] expected")
-    _need(Y, "Y", [None] * (Y.dim() - 1) + [N], (torch.bfloat16,))
+    _need(Y, "Y", (*Y.shape[:-1], N), (torch.bfloat16,))
     return Y.shape[0] if Y.dim() == 2 else Y.shape[0] * Y.shape[1]
 
 
 def combine(Y, row_of, out, weights=None, *, stream=None):
     """out[t] = sum_j weights[t, j] * Y[row_of[t, j]] (see moegg.h); weights None: all 1, which is also dispatch's
     backward pass.  Y bf16 [rows, N] or [G, cap, N], out bf16 [T, N], weights fp32 [T, k]."""
-    _need(out, "out", [None, None], (torch.bfloat16,))
-    T, N = out.shape
-    _need(row_of, "row_of", [T, None], (torch.int32,))
+    T, N = _matrix(out, "out", (torch.bfloat16,))
+    k = _top_k(row_of, "row_of", T)
     rows = _expert_rows(Y, N)
     if weights is not None:
-        _need(weights, "weights", list(row_of.shape), (torch.float32,))
+        _need(weights, "weights", (T, k), (torch.float32,))
     _one_device(Y, row_of, out, weights)
-    _check(lib().moegg_combine(_p(Y), _p(row_of), _p(weights), _p(out), T, row_of.shape[1], N, rows,
+    _check(lib().moegg_combine(_p(Y), _p(row_of), _p(weights), _p(out), T, k, N, rows,
                                _stream(stream)), "moegg_combine")
 
 
 def combine_backward(dout, Y, weights, row_of, dY, d_weights, dY_scale=None, *, scale_km: bool = False, stream=None):
     """dY[row_of[t, j]] = weights[t, j] * dout[t] in dY's operand format (as dispatch's A), and d_weights[t, j] =
     <Y[row_of[t, j]], dout[t]> (see moegg.h)."""
-    _need(dout, "dout", [None, None], (torch.bfloat16,))
-    T, N = dout.shape
-    _need(row_of, "row_of", [T, None], (torch.int32,))
-    _need(weights, "weights", list(row_of.shape), (torch.float32,))
-    _need(d_weights, "d_weights", list(row_of.shape), (torch.float32,))
+    T, N = _matrix(dout, "dout", (torch.bfloat16,))
+    k = _top_k(row_of, "row_of", T)
+    _need(weights, "weights", (T, k), (torch.float32,))
+    _need(d_weights, "d_weights", (T, k), (torch.float32,))
     rows, code = _row_operand(dY, "dY", dY_scale, N, scale_km)
     if _expert_rows(Y, N) != rows:
         raise ValueError(f"Y: shape {list(Y.shape)}, expected {rows} rows as dY")
     _one_device(dout, Y, weights, row_of, dY, d_weights, dY_scale)
     _check(lib().moegg_combine_backward(_p(dout), _p(Y), _p(weights), _p(row_of), _p(dY), _p(dY_scale), _p(d_weights),
-                                        T, row_of.shape[1], N, rows, code, _stream(stream)), "moegg_combine_backward")
+                                        T, k, N, rows, code, _stream(stream)), "moegg_combine_backward")
 
 
 def _no_e8m0(code: int, name: str):
@@ -714,8 +733,7 @@ def swiglu_checkpoint(GU, m_sizes, H, ckpt, ckpt_scale, H_scale=None, *, scale_k
     """H = silu(g) * u of GU bf16 [rows, 2I] (columns in interleave_gate_up's order), and GU kept as e4m3 ckpt
     [rows, 2I] with fp32 ckpt_scale [rows, 2I/128] (see moegg.h).  H bf16 [rows, I], or e4m3 with H_scale fp32
     [rows, I/128] ([I/128, rows] with scale_km)."""
-    _need(H, "H", [None, None], (torch.bfloat16, _E4M3))
-    rows, I = H.shape
+    rows, I = _matrix(H, "H", (torch.bfloat16, _E4M3))
     _, code = _row_operand(H, "H", H_scale, I, scale_km)
     _no_e8m0(code, "H_scale")
     _need(GU, "GU", [rows, 2 * I], (torch.bfloat16,))
@@ -729,8 +747,7 @@ def swiglu_checkpoint(GU, m_sizes, H, ckpt, ckpt_scale, H_scale=None, *, scale_k
 
 def swiglu_checkpoint_backward(dH, m_sizes, ckpt, ckpt_scale, dGU, H, *, stream=None):
     """dGU bf16 [rows, 2I] and H bf16 [rows, I] again, from dH bf16 [rows, I] and the checkpoint (see moegg.h)."""
-    _need(dH, "dH", [None, None], (torch.bfloat16,))
-    rows, I = dH.shape
+    rows, I = _matrix(dH, "dH", (torch.bfloat16,))
     _need(ckpt, "ckpt", [rows, 2 * I], (_E4M3,))
     _need(ckpt_scale, "ckpt_scale", [rows, 2 * I // 128], (torch.float32,))
     _need(dGU, "dGU", [rows, 2 * I], (torch.bfloat16,))
@@ -747,8 +764,7 @@ def swiglu_checkpoint_backward_fp8(dH, m_sizes, ckpt, ckpt_scale, dGU, dGU_scale
     """The operands of both gradients' products from dH bf16 [rows, I] and the checkpoint (see moegg.h): dGU e4m3
     [rows, 2I] with fp32 dGU_scale [rows, 2I/128] ([2I/128, rows] with scale_km); dGU_k e4m3 [rows, 2I] and H_k
     e4m3 [rows, I] with scales per token group, [S, 2I] and [S, I], fp32 or uint8 E8M0 bytes (k_scale_groups)."""
-    _need(dH, "dH", [None, None], (torch.bfloat16,))
-    rows, I = dH.shape
+    rows, I = _matrix(dH, "dH", (torch.bfloat16,))
     _need(ckpt, "ckpt", [rows, 2 * I], (_E4M3,))
     _need(ckpt_scale, "ckpt_scale", [rows, 2 * I // 128], (torch.float32,))
     _need(dGU, "dGU", [rows, 2 * I], (_E4M3,))
@@ -769,8 +785,7 @@ def swiglu_checkpoint_backward_fp8(dH, m_sizes, ckpt, ckpt_scale, dGU, dGU_scale
 def checkpoint_to_k_groups(X, m_sizes, X_k, X_k_scale, X_scale=None, *, scale_km: bool = False, stream=None):
     """A saved activation X [rows, M] (bf16, or e4m3 with fp32 scales [rows, M/128], [M/128, rows] with scale_km) as
     an operand of grouped_gemm_k_grouped: X_k e4m3 [rows, M] with X_k_scale [S, M], fp32 or uint8 E8M0 (see moegg.h)."""
-    _need(X, "X", [None, None], (torch.bfloat16, _E4M3))
-    rows, M = X.shape
+    rows, M = _matrix(X, "X", (torch.bfloat16, _E4M3))
     _, code = _row_operand(X, "X", X_scale, M, scale_km)
     _no_e8m0(code, "X_scale")
     _need(X_k, "X_k", [rows, M], (_E4M3,))
