@@ -11,6 +11,7 @@ not been built, `lib()` raises.  There is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import List, Optional, Sequence, Tuple
@@ -330,6 +331,7 @@ def _operands(rows: int, K: int, A, A_scale, B, B_scale, G: int, b_layout: int, 
     return (FP8_E4M3_SCALE_KM if scale_km else FP8_E4M3), N
 
 
+@functools.lru_cache(maxsize=64)
 def workspace_bytes(G: int, max_rows: int) -> int:
     return int(lib().moegg_workspace_bytes(G, max_rows))
 
@@ -581,6 +583,7 @@ def grouped_gemm_k_grouped(X, dY, dW, t_sizes, ws, X_scale=None, dY_scale=None, 
 # ---------------------------------------------------------------- the layer around the grouped GEMMs
 
 
+@functools.lru_cache(maxsize=64)
 def route_workspace_bytes(T: int, E: int) -> int:
     return int(lib().moegg_route_workspace_bytes(T, E))
 
@@ -622,12 +625,12 @@ def route(logits, ids, weights, m_sizes, row_of, ws, *, rows_total: int, bias=No
     (rows_total = E * cap); -1 where there is none.  ws: route_workspace(T, E)."""
     T, E, kind = _logits(logits)
     k = _top_k(ids, "ids", T)
-    _need(weights, "weights", [T, k], (torch.float32,))
-    _need(m_sizes, "m_sizes", [E], (torch.int32,))
-    _need(row_of, "row_of", [T, k], (torch.int32,))
+    _need(weights, "weights", (T, k), (torch.float32,))
+    _need(m_sizes, "m_sizes", (E,), (torch.int32,))
+    _need(row_of, "row_of", (T, k), (torch.int32,))
     if bias is not None:
-        _need(bias, "bias", [E], (torch.float32,))
-    _need(ws, "ws", [None], (torch.uint8,))
+        _need(bias, "bias", (E,), (torch.float32,))
+    _need(ws, "ws", (None,), (torch.uint8,))
     need = route_workspace_bytes(T, E)
     if ws.numel() < need:
         raise ValueError(f"ws: {ws.numel()} bytes, need {need} (route_workspace_bytes({T}, {E}))")
@@ -642,7 +645,7 @@ def route_backward(logits, ids, d_weights, d_logits, *, score: int = SCORE_SOFTM
     """d_logits [T, E] (logits' dtype) from d_weights [T, k] and the ids that route chose (see moegg.h)."""
     T, E, kind = _logits(logits)
     k = _top_k(ids, "ids", T)
-    _need(d_weights, "d_weights", [T, k], (torch.float32,))
+    _need(d_weights, "d_weights", (T, k), (torch.float32,))
     _need(d_logits, "d_logits", [T, E], (logits.dtype,))
     _one_device(logits, ids, d_weights, d_logits)
     _check(lib().moegg_route_backward(_p(logits), kind, _p(ids), _p(d_weights), _p(d_logits), T, E, k, score, renorm,
@@ -665,7 +668,7 @@ def _row_operand(A, name: str, A_scale, width: int, scale_km: bool) -> Tuple[int
     if isinstance(A_scale, torch.Tensor) and A_scale.dtype == torch.uint8:
         if scale_km:
             raise ValueError("scale_km applies to e4m3 operands with fp32 scales")
-        _need(A_scale, f"{name}_scale", [width // 128, rows], (torch.uint8,))
+        _need(A_scale, f"{name}_scale", (width // 128, rows), (torch.uint8,))
         return rows, FP8_E4M3_E8M0
     _need(A_scale, f"{name}_scale", [width // 128, rows] if scale_km else [*A.shape[:-1], width // 128],
           (torch.float32,))
@@ -725,7 +728,7 @@ def _no_e8m0(code: int, name: str):
 
 
 def _token_group_scales(X_scale, name: str, width: int, groups: Optional[int] = None, dtype=None) -> int:
-    _need(X_scale, name, [groups, width], (torch.float32, torch.uint8) if dtype is None else (dtype,))
+    _need(X_scale, name, (groups, width), (torch.float32, torch.uint8) if dtype is None else (dtype,))
     return X_scale.shape[0]
 
 
@@ -736,9 +739,9 @@ def swiglu_checkpoint(GU, m_sizes, H, ckpt, ckpt_scale, H_scale=None, *, scale_k
     rows, I = _matrix(H, "H", (torch.bfloat16, _E4M3))
     _, code = _row_operand(H, "H", H_scale, I, scale_km)
     _no_e8m0(code, "H_scale")
-    _need(GU, "GU", [rows, 2 * I], (torch.bfloat16,))
-    _need(ckpt, "ckpt", [rows, 2 * I], (_E4M3,))
-    _need(ckpt_scale, "ckpt_scale", [rows, 2 * I // 128], (torch.float32,))
+    _need(GU, "GU", (rows, 2 * I), (torch.bfloat16,))
+    _need(ckpt, "ckpt", (rows, 2 * I), (_E4M3,))
+    _need(ckpt_scale, "ckpt_scale", (rows, 2 * I // 128), (torch.float32,))
     _counts(m_sizes, "m_sizes")
     _one_device(GU, m_sizes, H, ckpt, ckpt_scale, H_scale)
     _check(lib().moegg_swiglu_checkpoint(_p(GU), _p(m_sizes), _p(H), _p(H_scale), _p(ckpt), _p(ckpt_scale),
@@ -748,10 +751,10 @@ def swiglu_checkpoint(GU, m_sizes, H, ckpt, ckpt_scale, H_scale=None, *, scale_k
 def swiglu_checkpoint_backward(dH, m_sizes, ckpt, ckpt_scale, dGU, H, *, stream=None):
     """dGU bf16 [rows, 2I] and H bf16 [rows, I] again, from dH bf16 [rows, I] and the checkpoint (see moegg.h)."""
     rows, I = _matrix(dH, "dH", (torch.bfloat16,))
-    _need(ckpt, "ckpt", [rows, 2 * I], (_E4M3,))
-    _need(ckpt_scale, "ckpt_scale", [rows, 2 * I // 128], (torch.float32,))
-    _need(dGU, "dGU", [rows, 2 * I], (torch.bfloat16,))
-    _need(H, "H", [rows, I], (torch.bfloat16,))
+    _need(ckpt, "ckpt", (rows, 2 * I), (_E4M3,))
+    _need(ckpt_scale, "ckpt_scale", (rows, 2 * I // 128), (torch.float32,))
+    _need(dGU, "dGU", (rows, 2 * I), (torch.bfloat16,))
+    _need(H, "H", (rows, I), (torch.bfloat16,))
     _counts(m_sizes, "m_sizes")
     _one_device(dH, m_sizes, ckpt, ckpt_scale, dGU, H)
     _check(lib().moegg_swiglu_checkpoint_backward(_p(dH), _p(m_sizes), _p(ckpt), _p(ckpt_scale), _p(dGU), _p(H),
@@ -765,13 +768,13 @@ def swiglu_checkpoint_backward_fp8(dH, m_sizes, ckpt, ckpt_scale, dGU, dGU_scale
     [rows, 2I] with fp32 dGU_scale [rows, 2I/128] ([2I/128, rows] with scale_km); dGU_k e4m3 [rows, 2I] and H_k
     e4m3 [rows, I] with scales per token group, [S, 2I] and [S, I], fp32 or uint8 E8M0 bytes (k_scale_groups)."""
     rows, I = _matrix(dH, "dH", (torch.bfloat16,))
-    _need(ckpt, "ckpt", [rows, 2 * I], (_E4M3,))
-    _need(ckpt_scale, "ckpt_scale", [rows, 2 * I // 128], (torch.float32,))
-    _need(dGU, "dGU", [rows, 2 * I], (_E4M3,))
+    _need(ckpt, "ckpt", (rows, 2 * I), (_E4M3,))
+    _need(ckpt_scale, "ckpt_scale", (rows, 2 * I // 128), (torch.float32,))
+    _need(dGU, "dGU", (rows, 2 * I), (_E4M3,))
     _, code = _row_operand(dGU, "dGU", dGU_scale, 2 * I, scale_km)
     _no_e8m0(code, "dGU_scale")
-    _need(dGU_k, "dGU_k", [rows, 2 * I], (_E4M3,))
-    _need(H_k, "H_k", [rows, I], (_E4M3,))
+    _need(dGU_k, "dGU_k", (rows, 2 * I), (_E4M3,))
+    _need(H_k, "H_k", (rows, I), (_E4M3,))
     S = _token_group_scales(dGU_k_scale, "dGU_k_scale", 2 * I)
     _token_group_scales(H_k_scale, "H_k_scale", I, S, dGU_k_scale.dtype)
     _counts(m_sizes, "m_sizes")
@@ -788,7 +791,7 @@ def checkpoint_to_k_groups(X, m_sizes, X_k, X_k_scale, X_scale=None, *, scale_km
     rows, M = _matrix(X, "X", (torch.bfloat16, _E4M3))
     _, code = _row_operand(X, "X", X_scale, M, scale_km)
     _no_e8m0(code, "X_scale")
-    _need(X_k, "X_k", [rows, M], (_E4M3,))
+    _need(X_k, "X_k", (rows, M), (_E4M3,))
     S = _token_group_scales(X_k_scale, "X_k_scale", M)
     _counts(m_sizes, "m_sizes")
     _one_device(X, X_scale, m_sizes, X_k, X_k_scale)

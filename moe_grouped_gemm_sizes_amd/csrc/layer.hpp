@@ -186,6 +186,13 @@ __device__ __forceinline__ float wave_sum(float v) {
     return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 
+// A barrier for what the workgroup shares in LDS: global accesses stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // ----------------------------------------------------------------- streams
 
 // Accesses to data that this kernel does not touch again: marked so that

@@ -17,6 +17,8 @@
 // adds the segment start and the earlier tiles.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "layer.hpp"
 
 namespace moegg {
@@ -78,9 +80,9 @@ __device__ __forceinline__ void scores64(const float (&l)[VPL], int sigmoid, dou
     for (int i = 0; i < VPL; ++i) s[i] *= r;
 }
 
-// Weights of the k chosen experts; lane j < k holds the j-th one's logit (-inf
-// where there is none).  lse-like terms of a softmax over all experts come
-// from the caller (top, z).
+// Weights of the k chosen experts; lane j < k holds the j-th one's
+// logit (-inf where there is none).  A softmax over all experts brings its
+// maximum and sum of exponentials (top, z).
 __device__ __forceinline__ float route_weight(float got, int sigmoid, int renorm, float scale, float top, float z) {
     const bool there = got > -__builtin_inff();
     if (!renorm) {
@@ -101,9 +103,9 @@ __device__ __forceinline__ float route_weight(float got, int sigmoid, int renorm
     return sum > 0.f ? scale * t / sum : 0.f;
 }
 
-// One token: picks into lane j's `id` (-1: none) and weight.  MODE 0: 32-bit
-// keys, no 64-bit scores; 1: 32-bit keys, groups by 64-bit scores; 2: 64-bit
-// keys (bias).  gbuf: E doubles of this wave (n_groups > 1).
+// One token: picks into lane j's `id` (-1: none) and weight.
+// MODE 0: 32-bit keys, no 64-bit scores; 1: 32-bit keys, groups by 64-bit
+// scores; 2: 64-bit keys (bias).  gbuf: E doubles of this wave (n_groups > 1).
 template <int VPL, int MODE>
 __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int lane, double* gbuf, uint32_t gs_magic,
                                             int lanes_lg, int& id, float& weight) {
@@ -223,56 +225,60 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int lane,
 }
 
 // Exclusive scan of the experts' aligned counts by one wave: total[e] -> start[e].
-__device__ void segment_starts(const int32_t* total, int64_t* start, int E, int seg_align, int cap, int lane) {
-    const int per = (E + 63) / 64, e0 = min(E, lane * per), e1 = min(E, e0 + per);
-    if (cap) {
-        for (int e = e0; e < e1; ++e) start[e] = (int64_t)e * cap;
-        return;
-    }
-    int64_t sum = 0;
-    for (int e = e0; e < e1; ++e) sum += ((int64_t)total[e] + seg_align - 1) / seg_align * seg_align;
-    int64_t incl = sum;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const int64_t o = __shfl_up(incl, off, 64);
-        if (lane >= off) incl += o;
-    }
-    int64_t at = incl - sum;
-    for (int e = e0; e < e1; ++e) {
-        start[e] = at;
-        at += ((int64_t)total[e] + seg_align - 1) / seg_align * seg_align;
+// Sums stop at 2^31 - 1, which no row reaches.
+constexpr uint32_t kNoRow = 0x7FFFFFFFu;
+__device__ __forceinline__ uint32_t sum_rows(uint32_t a, uint32_t b) { return min(a + b, kNoRow); }
+__device__ void segment_starts(const int32_t* total, uint32_t* start, int E, int seg_align, int cap, int lane) {
+    uint32_t before = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+        const int e = e0 + lane;
+        uint32_t m = e < E ? (uint32_t)total[e] : 0u;
+        if (cap) m = e < E ? (uint32_t)cap : 0u;
+        else if (seg_align > 1)
+            m = (uint32_t)min((uint64_t)kNoRow,
+                              (uint64_t)((m + (uint32_t)seg_align - 1) / (uint32_t)seg_align) * (uint32_t)seg_align);
+        uint32_t end = m;
+        end = sum_rows(end, dpp<DPP_SHR + 1>(0, end));
+        end = sum_rows(end, dpp<DPP_SHR + 2>(0, end));
+        end = sum_rows(end, dpp<DPP_SHR + 4>(0, end));
+        end = sum_rows(end, dpp<DPP_SHR + 8>(0, end));
+        end = sum_rows(end, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)end, DPP_BCAST15, 0xA, 0xF, false));
+        end = sum_rows(end, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)end, DPP_BCAST31, 0xC, 0xF, false));
+        const uint32_t above = (uint32_t)__shfl_up((int)end, 1, 64);
+        if (e < E) start[e] = sum_rows(before, lane ? above : 0u);
+        before = sum_rows(before, (uint32_t)__builtin_amdgcn_readlane((int)end, 63));
     }
 }
 
-__device__ __forceinline__ int32_t final_row(int64_t start, int64_t rank, int cap, int64_t rows_total) {
-    if (cap && rank >= cap) return -1;
-    return start + rank < rows_total ? (int32_t)(start + rank) : -1;
+__device__ __forceinline__ int32_t final_row(uint32_t start, uint32_t rank, int cap, int64_t rows_total) {
+    if (cap && rank >= (uint32_t)cap) return -1;
+    return start + rank < (uint32_t)rows_total ? (int32_t)(start + rank) : -1;   // both below 2^31
 }
 
 // Workgroup b routes tokens [b * tile_tokens, ...).  ONE: the only workgroup;
 // it also writes m_sizes and final rows.
 template <int VPL, int MODE, bool ONE>
 __global__ __launch_bounds__(1024) void route_kernel(RouteArgs a, uint32_t gs_magic, int lanes_lg) {
-    extern __shared__ double gbuf_all[];                 // E per wave (groups only)
+    extern __shared__ double gbuf_all[];                 // groups only: E per wave
     __shared__ unsigned long long mask_s[kRouteMaxExperts];
     __shared__ int32_t count_s[kRouteMaxExperts];
     __shared__ int16_t ids_s[kStep * kRouteMaxTopK];
-    __shared__ int64_t start_s[ONE ? kRouteMaxExperts : 1];
+    __shared__ uint32_t start_s[ONE ? kRouteMaxExperts : 1];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int waves = blockDim.x >> 6, E = a.E, k = a.k;
     const int t0 = ONE ? 0 : blockIdx.x * a.tile_tokens, t1 = ONE ? a.T : min(a.T, t0 + a.tile_tokens);
+    double* gbuf = gbuf_all + (a.n_groups > 1 ? wave * E : 0);
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         mask_s[e] = 0;
         count_s[e] = 0;
     }
-    __syncthreads();
+    lds_barrier();
     for (int ts = t0; ts < t1; ts += kStep) {
         const int n = min(kStep, t1 - ts);
         for (int i = wave; i < n; i += waves) {
             int id;
             float w;
-            route_token<VPL, MODE>(a, ts + i, lane, gbuf_all + (a.n_groups > 1 ? wave * E : 0), gs_magic, lanes_lg, id,
-                                   w);
+            route_token<VPL, MODE>(a, ts + i, lane, gbuf, gs_magic, lanes_lg, id, w);
             if (lane < k) {
                 const int64_t at = (int64_t)(ts + i) * k + lane;
                 a.ids[at] = id;
@@ -281,10 +287,10 @@ __global__ __launch_bounds__(1024) void route_kernel(RouteArgs a, uint32_t gs_ma
                 if (id >= 0) atomicOr(&mask_s[id], 1ull << i);
             }
         }
-        __syncthreads();
+        lds_barrier();
         if constexpr (ONE) {                             // one step holds every token
             for (int e = threadIdx.x; e < E; e += blockDim.x) count_s[e] = __popcll(mask_s[e]);
-            __syncthreads();
+            lds_barrier();
             break;
         }
         for (int x = threadIdx.x; x < n * k; x += blockDim.x) {
@@ -292,21 +298,22 @@ __global__ __launch_bounds__(1024) void route_kernel(RouteArgs a, uint32_t gs_ma
             if (id >= 0)
                 a.row_of[(int64_t)ts * k + x] = count_s[id] + __popcll(mask_s[id] & ((1ull << i) - 1));
         }
-        __syncthreads();
+        lds_barrier();
         for (int e = threadIdx.x; e < E; e += blockDim.x) {
             count_s[e] += __popcll(mask_s[e]);
             mask_s[e] = 0;
         }
-        __syncthreads();
+        lds_barrier();
     }
     if constexpr (ONE) {
         if (wave == 0) segment_starts(count_s, start_s, E, a.seg_align, a.cap, lane);
         for (int e = threadIdx.x; e < E; e += blockDim.x) a.m_sizes[e] = count_s[e];
-        __syncthreads();
+        lds_barrier();
         for (int x = threadIdx.x; x < a.T * k; x += blockDim.x) {
             const int id = ids_s[x], i = x / k;
             a.row_of[x] = id < 0 ? -1
-                                 : final_row(start_s[id], __popcll(mask_s[id] & ((1ull << i) - 1)), a.cap, a.rows_total);
+                                 : final_row(start_s[id], (uint32_t)__popcll(mask_s[id] & ((1ull << i) - 1)), a.cap,
+                                             a.rows_total);
         }
     } else {
         uint32_t* out = (uint32_t*)(a.tile_counts + (int64_t)blockIdx.x * ((E + 1) & ~1));
@@ -323,7 +330,7 @@ constexpr int kRowsThreads = 1024;
 __global__ __launch_bounds__(kRowsThreads) void route_rows_kernel(RouteArgs a, int tiles) {
     __shared__ int32_t total_s[kRouteMaxExperts];
     __shared__ int32_t before_s[kRouteMaxExperts];
-    __shared__ int64_t start_s[kRouteMaxExperts];
+    __shared__ uint32_t start_s[kRouteMaxExperts];
     const int E = a.E, pairs = (E + 1) / 2, b = blockIdx.x, k = a.k;
     for (int e = threadIdx.x; e < 2 * pairs; e += kRowsThreads) {
         total_s[e] = 0;
@@ -358,7 +365,7 @@ __global__ __launch_bounds__(kRowsThreads) void route_rows_kernel(RouteArgs a, i
     const int64_t x0 = (int64_t)b * a.tile_tokens * k, x1 = min((int64_t)a.T * k, x0 + (int64_t)a.tile_tokens * k);
     for (int64_t x = x0 + threadIdx.x; x < x1; x += kRowsThreads) {
         const int id = a.ids[x];
-        a.row_of[x] = id < 0 ? -1 : final_row(start_s[id], (int64_t)before_s[id] + a.row_of[x], a.cap, a.rows_total);
+        a.row_of[x] = id < 0 ? -1 : final_row(start_s[id], (uint32_t)before_s[id] + (uint32_t)a.row_of[x], a.cap, a.rows_total);
     }
 }
 
@@ -443,17 +450,18 @@ static hipError_t route_as(const RouteArgs& a, hipStream_t s) {
         magic = (uint32_t)(0xFFFFFFFFull / (uint32_t)(a.E / a.n_groups)) + 1u;
         while ((a.n_groups << (lg + 1)) <= 64) ++lg;
     }
-    const bool one = a.T <= kStep;
     // with groups, a wave has E doubles of LDS: at most 32 KB for all of them
     const int most = a.n_groups == 1 || a.E <= 256 ? 16 : (a.E <= 512 ? 8 : 4);
-    const int tokens = one ? a.T : (a.tile_tokens < kStep ? a.tile_tokens : kStep);
-    const int waves = tokens < 4 ? 4 : (tokens < most ? tokens : most);
-    const size_t lds = a.n_groups > 1 ? sizeof(double) * (size_t)a.E * waves : 0;
-    if (one) {
-        route_kernel<VPL, MODE, true><<<1, waves * 64, lds, s>>>(a, magic, lg);
+    if (a.T <= kStep) {
+        const int waves = a.T < 4 ? 4 : (a.T < most ? a.T : most);
+        route_kernel<VPL, MODE, true>
+            <<<1, waves * 64, a.n_groups > 1 ? sizeof(double) * (size_t)a.E * waves : 0, s>>>(a, magic, lg);
         return hipGetLastError();
     }
     const int tiles = (a.T + a.tile_tokens - 1) / a.tile_tokens;
+    const int tokens = a.tile_tokens < kStep ? a.tile_tokens : kStep;
+    const int waves = std::min(tokens, most);
+    const size_t lds = a.n_groups > 1 ? sizeof(double) * (size_t)a.E * waves : 0;
     route_kernel<VPL, MODE, false><<<tiles, waves * 64, lds, s>>>(a, magic, lg);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
