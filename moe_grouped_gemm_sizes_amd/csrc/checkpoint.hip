@@ -292,6 +292,9 @@ __device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t rs, uint32
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)off, (int)soff, CP_NT));
 }
 
+// Past the end of every buffer here (2^31 bytes at most), and no step added to it wraps.
+constexpr uint32_t kOutOfRange = 0x80000000u;
+
 template <OperandFormat FMT, bool E8M0>
 __global__ __launch_bounds__(kThreads) void swiglu_backward_fp8_kernel(CheckpointArgs a) {
     constexpr int C = kBwdCols + kBwdCols / 2;           // columns of dGU (in lane order), then of H
@@ -331,7 +334,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_fp8_kernel(Checkpoin
         auto out = make_rsrc((const uint8_t*)a.row_out + u * kBwdCols, units * kBwdCols);
         auto out_scale = FMT == kRows ? make_rsrc((const float*)a.row_scale + u, units * 4)
                                       : make_rsrc((const float*)a.row_scale + (int64_t)unit * a.rows + tg.row, tg.n * 4);
-        const int scale_at = l8 ? -1 : (FMT == kRows ? (int)(at * 4) : r0 * 4);   // -1: out of range
+        const uint32_t scale_at = l8 ? kOutOfRange : (FMT == kRows ? at * 4 : (uint32_t)r0 * 4);
         const int scale_step = FMT == kRows ? upr * 4 : 4;
 #pragma unroll
         for (int p = 0; p < kBwdPasses; ++p) {
@@ -341,7 +344,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_fp8_kernel(Checkpoin
             quantize<16>(v[p], g, q);
             __builtin_amdgcn_raw_buffer_store_b128(join_codes(u32x2{q[0], q[1]}, u32x2{q[2], q[3]}, odd), out,
                                                    (int)(at * kBwdCols + l8 * 16), p * kBwdRows * upr * kBwdCols, CP_NT);
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(g.s), out_scale, scale_at, p * kBwdRows * scale_step, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(g.s), out_scale, (int)scale_at, p * kBwdRows * scale_step, 0);
             __builtin_amdgcn_sched_barrier(0);           // one pass's temporaries at a time
         }
     }

@@ -76,7 +76,8 @@ moegg_status_t check_operand(const void* p, const void* scale, int64_t rows, int
     return W % kGroup == 0 ? MOEGG_OK : MOEGG_ERR_UNSUPPORTED;
 }
 
-// Shared by the checkpoint calls: counts, rows, width (a multiple of `unit`) and grid.
+// Shared by the checkpoint calls: counts, rows, width (a multiple of `unit`) and
+// grid, `threads` work-items for each token group and unit.
 moegg_status_t check_checkpoint(const int32_t* m_sizes, int G, int64_t rows, int W, int unit, int64_t threads) {
     if (!m_sizes || !aligned(m_sizes, 4) || G < 1 || G > kMaxExperts || rows < 0 || rows > INT32_MAX || W < 1)
         return MOEGG_ERR_INVALID_ARG;
@@ -237,7 +238,7 @@ moegg_status_t moegg_combine_backward(const void* dout, const void* Y, const flo
 moegg_status_t moegg_swiglu_checkpoint(const void* GU, const int32_t* m_sizes, void* H, void* H_scale, void* ckpt,
                                        float* ckpt_scale, int G, int64_t rows_total, int I, moegg_dtype_t dtype,
                                        void* stream) {
-    moegg_status_t st = check_checkpoint(m_sizes, G, rows_total, I, 128, 256);
+    moegg_status_t st = check_checkpoint(m_sizes, G, rows_total, I, 128, 16 * 128);
     if (st != MOEGG_OK) return st;
     CheckpointArgs a{};
     if (!format_of(dtype, &a.fmt)) return MOEGG_ERR_INVALID_ARG;
@@ -260,7 +261,7 @@ moegg_status_t moegg_swiglu_checkpoint(const void* GU, const int32_t* m_sizes, v
 moegg_status_t moegg_swiglu_checkpoint_backward(const void* dH, const int32_t* m_sizes, const void* ckpt,
                                                 const float* ckpt_scale, void* dGU, void* H, int G,
                                                 int64_t rows_total, int I, void* stream) {
-    moegg_status_t st = check_checkpoint(m_sizes, G, rows_total, I, 128, 256);
+    moegg_status_t st = check_checkpoint(m_sizes, G, rows_total, I, 128, 16 * 128);
     if (st != MOEGG_OK) return st;
     if (rows_total > 0 && any_null({dH, ckpt, ckpt_scale, dGU, H})) return MOEGG_ERR_INVALID_ARG;
     if (!all16({dH, ckpt, dGU, H}) || !all4({ckpt_scale})) return MOEGG_ERR_INVALID_ARG;

@@ -577,6 +577,56 @@ def test_many_experts_token_groups():
     check_token_groups(X_k, ks, f64(x), U * np.abs(f64(x)), counts, rows, False)
 
 
+def test_checkpoint_offsets_past_32_bits():
+    """The last rows of buffers of 4 to 9 GB come out as a call on those rows alone computes them, bit for bit."""
+    rows, tail, I = 540_000, 300, 4096
+    counts = [rows - tail, 0, tail]
+    m, m_tail = (torch.tensor(c, dtype=torch.int32).cuda() for c in (counts, [tail]))
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    last = slice(rows - tail, rows)
+
+    def same(a, b):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+    def forward(gu, m_sizes):
+        n = gu.shape[0]
+        H, hs = operand((n,), n, I, "km")
+        ck, cs = operand((n,), n, 2 * I, "rows")
+        mg.swiglu_checkpoint(gu, m_sizes, H, ck, cs, hs, scale_km=True)
+        return H, hs, ck, cs
+
+    def backward(dh, m_sizes, ck, cs):
+        n, S = dh.shape[0], mg.k_scale_groups(m_sizes.tolist())
+        dGU, ds = operand((n,), n, 2 * I, "km")
+        dk, dks, hk, hks = buf((n, 2 * I), E4M3), buf((S, 2 * I), torch.float32), buf((n, I), E4M3), buf((S, I), torch.float32)
+        mg.swiglu_checkpoint_backward_fp8(dh, m_sizes, ck, cs, dGU, ds, dk, dks, hk, hks, scale_km=True)
+        return dGU, ds, dk, dks, hk, hks
+
+    gu = torch.empty(rows, 2 * I, dtype=BF16, device="cuda").normal_(generator=g)
+    H, hs, ck, cs = forward(gu, m)
+    h, hs1, c, cs1 = forward(gu[last].contiguous(), m_tail)
+    same(H[last], h), same(hs[:, last], hs1), same(ck[last], c), same(cs[last], cs1)
+    del gu, H, hs, h, hs1
+    dh = torch.empty(rows, I, dtype=BF16, device="cuda").normal_(generator=g)
+    big, small = backward(dh, m, ck, cs), backward(dh[last].contiguous(), m_tail, c, cs1)
+    groups = small[3].shape[0]
+    for i in (0, 2, 4):
+        same(big[i][last], small[i])
+    same(big[1][:, last], small[1]), same(big[3][-groups:], small[3]), same(big[5][-groups:], small[5])
+    del big, small
+    dGU, H2 = buf((rows, 2 * I), BF16), buf((rows, I), BF16)
+    d1, h1 = buf((tail, 2 * I), BF16), buf((tail, I), BF16)
+    mg.swiglu_checkpoint_backward(dh, m, ck, cs, dGU, H2)
+    mg.swiglu_checkpoint_backward(dh[last].contiguous(), m_tail, c, cs1, d1, h1)
+    same(dGU[last], d1), same(H2[last], h1)
+    X_k, ks, x1, k1 = buf((rows, 2 * I), E4M3), buf((mg.k_scale_groups(counts), 2 * I), torch.uint8), buf((tail, 2 * I), E4M3), \
+        buf((groups, 2 * I), torch.uint8)
+    mg.checkpoint_to_k_groups(dGU, m, X_k, ks)
+    mg.checkpoint_to_k_groups(d1, m_tail, x1, k1)
+    same(X_k[last], x1), same(ks[-groups:], k1)
+
+
 # ------------------------------------------------------------------ streams, graphs
 
 def layer_step(s, stream=None):

@@ -103,7 +103,7 @@ def test_combine_backward_refusals(kw, status):
 
 CKPT_BAD = [(dict(m_sizes=None), INV), (dict(m_sizes=ODD), INV), (dict(G=0), INV), (dict(G=4097), INV),
             (dict(rows=-1), INV), (dict(rows=1 << 31), INV), (dict(I=0), INV), (dict(I=192), UNS),
-            (dict(rows=1 << 30, I=1 << 20), UNS)]
+            (dict(rows=1 << 30, I=1 << 20), UNS), (dict(I=1 << 22), UNS)]
 FWD = dict(GU=FAKE, m_sizes=FAKE, H=FAKE, H_scale=FAKE, ckpt=FAKE, ckpt_scale=FAKE, G=8, rows=100, I=256,
            dtype=mg.FP8_E4M3)
 
@@ -112,6 +112,7 @@ FWD = dict(GU=FAKE, m_sizes=FAKE, H=FAKE, H_scale=FAKE, ckpt=FAKE, ckpt_scale=FA
     (dict(GU=None), INV), (dict(H=None), INV), (dict(H_scale=None), INV), (dict(ckpt=None), INV),
     (dict(ckpt_scale=None), INV), (dict(GU=EIGHT), INV), (dict(ckpt=EIGHT), INV), (dict(H_scale=ODD), INV),
     (dict(dtype=mg.FP8_E4M3_E8M0), UNS), (dict(dtype=8), INV),
+    (dict(rows=1 << 24, I=2048), UNS),                     # more work-items than a launch counts
 ])
 def test_swiglu_checkpoint_refusals(kw, status):
     assert call("moegg_swiglu_checkpoint", FWD, kw) == status
