@@ -53,7 +53,8 @@ __device__ __forceinline__ void unpack8(u32x4 v, float* f) {
 
 // ----------------------------------------------------------------- dispatch
 
-// bf16: a wave copies 512 elements of a token to its k rows.
+// bf16: a wave copies 512 elements of a token to its k rows.  4096 tokens of
+// 7168 to 8 experts each: 107 us, 4.9 TB/s of one read and 8 writes.
 __global__ __launch_bounds__(kThreads) void dispatch_bf16_kernel(PermuteArgs a, int chunks) {
     const int64_t item = wave_item();
     if (item >= (int64_t)a.T * chunks) return;
@@ -69,7 +70,10 @@ __global__ __launch_bounds__(kThreads) void dispatch_bf16_kernel(PermuteArgs a, 
 }
 
 // e4m3: a wave quantizes 1024 elements (8 groups) of a token, 16 a lane, and
-// stores them to its k rows.
+// stores them to its k rows.  The same 4096 tokens: 57 us with row-major scales
+// (5.3 TB/s), 64 us with transposed ones.  Those are 4 bytes to a line each, 1.8
+// million of them; giving an XCD neighbouring tokens or neighbouring columns
+// (whole lines then merge in its L2) makes no difference.
 template <OperandFormat FMT>
 __global__ __launch_bounds__(kThreads) void dispatch_fp8_kernel(PermuteArgs a, int chunks) {
     const int64_t item = wave_item();
@@ -116,7 +120,9 @@ __global__ __launch_bounds__(kThreads) void dispatch_fp8_kernel(PermuteArgs a, i
 // ----------------------------------------------------------------- combine
 
 // A wave sums 512 columns of a token's rows in fp32, in the order of its
-// assignments, and rounds once.  Eight rows are in flight at a time.
+// assignments, and rounds once.  Eight rows are in flight at a time.  32768 rows
+// of 7168 into 4096 tokens: 88 us, 6.0 TB/s; with cached accesses and each XCD on
+// an eighth of the tokens 107 us.
 __global__ __launch_bounds__(kThreads) void combine_kernel(PermuteArgs a, int chunks) {
     const int64_t item = wave_item();
     if (item >= (int64_t)a.T * chunks) return;
@@ -158,7 +164,9 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(PermuteArgs a, int ch
 
 // A workgroup takes a token: dY rows are weight * dout, and each weight's
 // gradient is the dot product of its row of Y with dout, summed in fp32 in a
-// fixed order (lane pieces, wave, waves).  dout is read once per 8 rows.
+// fixed order (lane pieces, wave, waves).  dout is read once per 8 rows.  32768
+// rows of 7168 in bf16: 189 us, 5.3 TB/s, and 158 us with e4m3 dY; as many
+// waves as there are 512-column pieces, since 4 waves going round take 202 us.
 template <OperandFormat FMT>
 __global__ __launch_bounds__(1024) void combine_backward_kernel(PermuteArgs a) {
     __shared__ float part_s[16][8];
@@ -265,7 +273,7 @@ hipError_t launch_combine(const PermuteArgs& a, hipStream_t s) {
 
 hipError_t launch_combine_backward(const PermuteArgs& a, hipStream_t s) {
     if (a.T == 0) return hipSuccess;
-    // a wave for each 512 columns, up to 16: 14 waves on 7168 columns take 189 us where 4 take 202
+    // a wave for each 512 columns, up to 16
     const int threads = 64 * (a.W >= 16 * 512 ? 16 : (a.W + 511) / 512);
     switch (a.fmt) {
         case kBf16: combine_backward_kernel<kBf16><<<a.T, threads, 0, s>>>(a); break;
