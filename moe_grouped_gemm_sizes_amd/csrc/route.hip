@@ -25,6 +25,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "layer.hpp"
 
@@ -43,6 +44,26 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i, int bf16) 
     return bf16 ? __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16) : ((const float*)p)[i];
 }
 
+// The lane's logits of token t, -inf past the experts.  All loads are issued
+// before any is used: no branch between them (lanes past the end read the last one).
+template <int VPL>
+__device__ __forceinline__ void load_logits(const void* logits, int64_t t, int E, int bf16, int lane, float (&l)[VPL]) {
+    if (bf16) {
+        const uint16_t* p = (const uint16_t*)logits + t * E;
+        uint16_t r[VPL];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) r[i] = p[min(lane + 64 * i, E - 1)];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) l[i] = __uint_as_float((uint32_t)r[i] << 16);
+    } else {
+        const float* p = (const float*)logits + t * E;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) l[i] = p[min(lane + 64 * i, E - 1)];
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) l[i] = lane + 64 * i < E ? clean_logit(l[i]) : -__builtin_inff();
+}
+
 // Unsigned integers in the order of the floats.
 __device__ __forceinline__ uint32_t key32(float f) {
     const uint32_t b = __float_as_uint(f);
@@ -51,6 +72,16 @@ __device__ __forceinline__ uint32_t key32(float f) {
 __device__ __forceinline__ uint64_t key64(double d) {
     const uint64_t b = (uint64_t)__double_as_longlong(d);
     return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+}
+
+__device__ __forceinline__ float unkey32(uint32_t k) {
+    return __uint_as_float(k ^ (~(uint32_t)((int32_t)k >> 31) | 0x80000000u));
+}
+template <typename T>
+__device__ __forceinline__ void swap_if(bool c, T& a, T& b) {
+    const T x = c ? b : a, y = c ? a : b;
+    a = x;
+    b = y;
 }
 
 __device__ __forceinline__ double wave_sum_f64(double v) {
@@ -118,22 +149,21 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int lane,
                                             int lanes_lg, int& id, float& weight) {
     const int E = a.E, k = a.k;
     constexpr float ninf = -__builtin_inff();
-    float l[VPL];
+    float l[VPL], bias[VPL];
+    if constexpr (MODE == 2) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int e = lane + 64 * i;
-        l[i] = e < E ? clean_logit(load_logit(a.logits, (int64_t)t * E + e, a.bf16)) : ninf;
+        for (int i = 0; i < VPL; ++i) bias[i] = a.bias[min(lane + 64 * i, E - 1)];
     }
+    load_logits<VPL>(a.logits, t, E, a.bf16, lane, l);
     double s[MODE ? VPL : 1];
     if constexpr (MODE != 0) scores64<VPL>(l, a.sigmoid, s);
     uint32_t hi[VPL], lo[MODE == 2 ? VPL : 1];       // keys, 0: not to be picked
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-        const int e = lane + 64 * i;
         if constexpr (MODE == 2) {
-            const float b = e < E ? a.bias[e] : ninf;
+            const float b = clean_logit(bias[i]);        // NaN, -inf: not to be chosen
             const bool there = l[i] > ninf && b > ninf;
-            s[i] = there ? s[i] + (double)fminf(b, kFltMax) : -__builtin_inf();
+            s[i] = there ? s[i] + (double)b : -__builtin_inf();
             const uint64_t key = there ? key64(s[i]) : 0;
             hi[i] = (uint32_t)(key >> 32);
             lo[i] = (uint32_t)key;
@@ -189,30 +219,85 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int lane,
     }
     id = -1;
     float got = ninf;
-    for (int j = 0; j < k; ++j) {
-        uint32_t m = hi[0];
-#pragma unroll
-        for (int i = 1; i < VPL; ++i) m = max(m, hi[i]);
-        m = wave_max_u32(m);
-        if (m == 0) break;                               // nothing left: the same for every lane
-        uint32_t ml = 0;
-        if constexpr (MODE == 2) {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) ml = max(ml, hi[i] == m ? lo[i] : 0u);
-            ml = wave_max_u32(ml);
-        }
-        bool found = false;
+    if constexpr (VPL <= 4) {
+        // The lane's keys in descending order (equal ones by id: only strictly smaller keys move back), so that a
+        // pick looks at one key a lane and its holder moves up the others.
+        typedef typename std::conditional<MODE == 2, uint64_t, uint32_t>::type Key;
+        Key key[VPL];
+        int e[VPL], left = 0;                            // left: experts that can be picked
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            bool mine = hi[i] == m;
-            if constexpr (MODE == 2) mine = mine && lo[i] == ml;
-            const uint64_t who = __ballot(mine);
-            if (!found && who) {
-                found = true;
-                const int src = __builtin_ctzll(who);
-                const float gv = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(l[i]), src));
-                if (lane == j) { id = src + 64 * i; got = gv; }
-                if (lane == src) hi[i] = 0;
+            e[i] = lane + 64 * i;
+            if constexpr (MODE == 2) key[i] = (uint64_t)hi[i] << 32 | lo[i];
+            else key[i] = hi[i];
+            left += __popcll(__ballot(hi[i] != 0));
+        }
+#pragma unroll
+        for (int n = VPL - 1; n > 0; --n) {
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const bool less = key[i] < key[i + 1];
+                swap_if(less, key[i], key[i + 1]);
+                swap_if(less, e[i], e[i + 1]);
+            }
+        }
+        const int picks = min(k, left);
+        for (int j = 0; j < picks; ++j) {
+            const uint32_t top = (uint32_t)(key[0] >> (MODE == 2 ? 32 : 0));
+            const uint32_t m = wave_max_u32(top);
+            uint64_t who = __ballot(top == m);
+            if constexpr (MODE == 2) {
+                if (who & (who - 1)) {
+                    const uint32_t low = wave_max_u32(top == m ? (uint32_t)key[0] : 0u);
+                    who = __ballot(top == m && (uint32_t)key[0] == low);
+                }
+            }
+            int src = __builtin_ctzll(who);
+            if constexpr (VPL > 1) {
+                if (who & (who - 1))                     // equal keys: the lowest id
+                    src = (int)(~wave_max_u32((who >> lane) & 1 ? ~(uint32_t)e[0] : 0u) & 63u);
+            }
+            const int ej = VPL > 1 ? __builtin_amdgcn_readlane(e[0], src) : src;
+            id = lane == j ? ej : id;
+            if constexpr (MODE != 2) got = lane == j ? unkey32(m) : got;
+            if (lane == src) {
+#pragma unroll
+                for (int i = 0; i + 1 < VPL; ++i) {
+                    key[i] = key[i + 1];
+                    e[i] = e[i + 1];
+                }
+                key[VPL - 1] = 0;
+            }
+        }
+        if constexpr (MODE == 2) {
+            if (id >= 0) got = clean_logit(load_logit(a.logits, (int64_t)t * E + id, a.bf16));
+        }
+    } else {
+        for (int j = 0; j < k; ++j) {
+            uint32_t m = hi[0];
+#pragma unroll
+            for (int i = 1; i < VPL; ++i) m = max(m, hi[i]);
+            m = wave_max_u32(m);
+            if (m == 0) break;                               // nothing left: the same for every lane
+            uint32_t ml = 0;
+            if constexpr (MODE == 2) {
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) ml = max(ml, hi[i] == m ? lo[i] : 0u);
+                ml = wave_max_u32(ml);
+            }
+            bool found = false;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                bool mine = hi[i] == m;
+                if constexpr (MODE == 2) mine = mine && lo[i] == ml;
+                const uint64_t who = __ballot(mine);
+                if (!found && who) {
+                    found = true;
+                    const int src = __builtin_ctzll(who);
+                    const float gv = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(l[i]), src));
+                    if (lane == j) { id = src + 64 * i; got = gv; }
+                    if (lane == src) hi[i] = 0;
+                }
             }
         }
     }
@@ -399,12 +484,9 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackwardArgs a
     float p[VPL], top = 0.f, z = 1.f;
     if (full) {
         float m = ninf;
+        load_logits<VPL>(a.logits, t, E, a.bf16, lane, p);
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const int e = lane + 64 * i;
-            p[i] = e < E ? clean_logit(load_logit(a.logits, t * E + e, a.bf16)) : ninf;
-            m = fmaxf(m, p[i]);
-        }
+        for (int i = 0; i < VPL; ++i) m = fmaxf(m, p[i]);
         m = wave_max(m);
         top = m > ninf ? m : 0.f;
         float sum = 0.f;
