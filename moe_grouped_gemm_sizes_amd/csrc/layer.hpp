@@ -22,7 +22,7 @@ struct RouteArgs {
     float* weights;                      // [T, k]
     int32_t* m_sizes;                    // [E]
     int32_t* row_of;                     // [T, k]
-    uint16_t* tile_counts;               // [tiles, E rounded up to 2]: assignments of each token tile
+    uint16_t* tile_counts;               // [tiles, route_count_width(E)]: assignments of each token tile
     int T, E, k;
     int bf16;                            // logits' type
     int sigmoid, renorm;
@@ -87,11 +87,16 @@ hipError_t launch_swiglu_checkpoint_backward(const CheckpointArgs& a, hipStream_
 hipError_t launch_swiglu_checkpoint_backward_fp8(const CheckpointArgs& a, hipStream_t s);
 hipError_t launch_checkpoint_to_k_groups(const CheckpointArgs& a, hipStream_t s);
 
-// Tokens of one workgroup of a routing call: a multiple of 16, at most 256 workgroups.
+// Tokens of one workgroup of a routing call: 4 (a wave on each SIMD) as long as
+// that makes at most 256 workgroups, then in steps of 4 up to a wave each, then of
+// 16.  64 tokens over 256 experts in groups: 10.5 us in tiles of 4, 14 us in tiles of 16.
 inline int route_tile_tokens(int T) {
     const int t = (T + kRouteMaxTiles - 1) / kRouteMaxTiles;
-    return t <= 16 ? 16 : (t + 15) / 16 * 16;
+    return t <= 4 ? 4 : (t <= 16 ? (t + 3) / 4 * 4 : (t + 15) / 16 * 16);
 }
+
+// Counts of one tile: 16 bits for every expert, in whole 16 bytes.
+constexpr int route_count_width(int E) { return (E + 7) & ~7; }
 
 #ifdef __HIPCC__
 

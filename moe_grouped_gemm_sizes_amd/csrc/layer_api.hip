@@ -110,7 +110,7 @@ extern "C" {
 size_t moegg_route_workspace_bytes(int T, int E) {
     if (T < 0 || T > kRouteMaxTokens || E < 1 || E > kRouteMaxExperts) return 0;
     const size_t tiles = ((size_t)T + route_tile_tokens(T) - 1) / route_tile_tokens(T);
-    return align256(std::max<size_t>(tiles, 1) * sizeof(uint16_t) * (size_t)((E + 1) & ~1));
+    return align256(std::max<size_t>(tiles, 1) * sizeof(uint16_t) * (size_t)route_count_width(E));
 }
 
 moegg_status_t moegg_route(const void* logits, moegg_logits_t logits_dtype, const float* bias, int32_t* ids,

@@ -198,6 +198,44 @@ def test_route_long_call_is_deterministic_and_counts_up():
     assert np.array_equal(a["row_of"].cpu().numpy().reshape(-1), row)
 
 
+@pytest.mark.parametrize("T,E,n", [(16, 96, 1), (17, 96, 3), (255, 256, 8), (1024, 40, 1), (1025, 129, 1), (2500, 512, 8),
+                                   (3500, 260, 2), (4097, 64, 4)])
+def test_route_sizes_around_the_tiles(T, E, n):
+    l = torch.randn(T, E, generator=gen(T)).to(BF16).cuda()
+    bias = (torch.randn(E, generator=gen(E)) * 0.1).cuda() if E % 64 == 0 else None
+    check_route(l, 4, 4 * T + 64 * E, bias=bias, score="sigmoid", n_groups=n, topk_groups=max(1, n // 2),
+                group_top=min(2, n), seg_align=16)
+
+
+@pytest.mark.parametrize("E", [64, 128, 160, 256, 384, 1024])
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+def test_route_rows_off_any_wider_alignment(E, dtype):
+    """Logits that begin one element into their storage; so do the gradient's."""
+    T, k = 20, 6
+    back = torch.randn(1 + T * E, generator=gen(E)).to(dtype).cuda()
+    l = back[1:].view(T, E)
+    _, ids = check_route(l, k, T * k)
+    dw = torch.randn(T, k, generator=gen(5))
+    ids = torch.tensor(ids, dtype=torch.int32).cuda()
+    a, b = torch.full((2 + T * E,), 7.0, dtype=dtype, device="cuda"), buf((T, E), dtype)
+    for renorm in (True, False):
+        mg.route_backward(l, ids, dw.cuda(), a[1:-1].view(T, E), renorm=renorm)
+        mg.route_backward(l.clone(), ids, dw.cuda(), b, renorm=renorm)
+        assert torch.equal(a[1:-1].view(T, E), b) and a[0] == 7 and a[-1] == 7
+
+
+@pytest.mark.parametrize("T,E,k", [(70001, 24, 3), (65535, 9, 2), (65536, 9, 2)])
+def test_route_rows_past_16_bit_counts(T, E, k):
+    """An expert's assignments below and above 2^16."""
+    l = torch.randn(T, E, generator=gen(T))
+    l[:, 3] += 20                                          # every token's first choice
+    got = run_route(l.cuda(), k, T * k)
+    ids = got["ids"].cpu().numpy()
+    m, row = ol.rows_of(ids, E, T * k, 1, 0)
+    assert (ids[:, 0] == 3).all() and m[3] == T
+    assert np.array_equal(got["m_sizes"].cpu().numpy(), m) and np.array_equal(got["row_of"].cpu().numpy(), row)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [True, False])
 @pytest.mark.parametrize("T,E,k,dtype", [(1, 1, 1, "float32"), (5, 64, 8, "float32"), (33, 160, 6, "bfloat16"),
