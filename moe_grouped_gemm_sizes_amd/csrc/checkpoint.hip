@@ -302,8 +302,9 @@ __device__ __forceinline__ void quantize_columns(const float* v, const float* pr
 constexpr int kBwdCols = 128, kBwdRows = kThreads / 8, kBwdPasses = 128 / kBwdRows;
 constexpr int kBwdRun = 16;
 
+template <bool ONCE = true>
 __device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t soff) {
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)off, (int)soff, CP_NT));
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)off, (int)soff, ONCE ? CP_NT : 0));
 }
 
 // Past the end of every buffer here (2^31 bytes at most), and no step added to it wraps.
@@ -421,7 +422,8 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_fp8_kernel(Checkpoin
 // times.  The codes (or bf16 values) stay in registers as they were read, and
 // are scaled twice: for the columns' maxima and for the new codes.  32768 rows of
 // 7168 columns: 89 us, 5.4 TB/s (cached accesses: 94 us; values kept in fp32
-// between the two: 100 us).
+// between the two: 100 us).  bf16 loads are not streamed: each takes the halves of
+// lines, which would then be fetched twice (4096 columns: 75 us, 82 us streamed).
 constexpr int kKgRows = kThreads / 16, kKgPasses = 128 / kKgRows, kKgRun = 8;
 
 template <OperandFormat FMT, bool E8M0>
@@ -453,7 +455,7 @@ __global__ __launch_bounds__(kThreads) void k_groups_kernel(CheckpointArgs a) {
             const uint32_t step = (uint32_t)(p * kKgRows);
 #pragma unroll
             for (int i = 0; i < RAW; ++i)
-                raw[p][i] = buffer_load16(in, (at * kUnit + l16 * 16) * RAW + i * 16, step * upr * kUnit * RAW);
+                raw[p][i] = buffer_load16<FMT != kBf16>(in, (at * kUnit + l16 * 16) * RAW + i * 16, step * upr * kUnit * RAW);
             scale[p] = 0.f;
             if (FMT == kRows)
                 scale[p] = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(

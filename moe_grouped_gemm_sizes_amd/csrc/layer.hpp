@@ -244,13 +244,11 @@ __device__ __forceinline__ void e4m3_to_f32(uint32_t v, float* f) {
 }
 
 // One group's scale amax / 448 (1 where that is 0; POW2: the smallest power of
-// two that is at least it, from 2^-126 up, as value and E8M0 byte) and pre and
-// inv, what values are multiplied with to become codes; pre is 1 but for scales
-// whose reciprocal may overflow.  With the hardware's reciprocal
-// (1 ulp) x * (1 / s) is within 2 ulp of x / s: it moves a code only where x / s is
-// that near a rounding border.
+// two that is at least it, from 2^-126 up, as value and E8M0 byte) and what turns
+// values into codes: pre, which is 1 but for scales whose reciprocal may
+// overflow, the reciprocal inv of the divisor s * pre, and what that is short of it.
 struct GroupScale {
-    float s, pre, inv;
+    float s, pre, inv, low;
     uint32_t byte;
 };
 constexpr float kTinyScale = 0x1p-100f;
@@ -272,32 +270,49 @@ __device__ __forceinline__ GroupScale group_scale(float amax) {
         g.byte = e;
         g.s = __uint_as_float(e << 23);
         g.inv = e == 255u ? 0.f : __uint_as_float((254u - e) << 23);
+        g.low = 0.f;
     } else {
         if (g.s < kTinyScale) g.pre = 0x1p+100f;
-        g.inv = __builtin_amdgcn_rcpf(g.s * g.pre);
+        const float d = g.s * g.pre;
+        g.inv = __builtin_amdgcn_rcpf(d);
+        g.low = d < __builtin_inff() ? __builtin_fmaf(-d, g.inv, 1.f) * g.inv : 0.f;
     }
     return g;
 }
 
+// x / s.  The product with the hardware's reciprocal (1 ulp) is within 2 ulp;
+// EXACT adds the rest of the reciprocal before it rounds, which leaves 2^-45: in
+// effect the rounded quotient.  bf16 values against a bf16 maximum meet e4m3's
+// rounding borders exactly (one value in two hundred of normal data), and there the
+// last bit decides the code; fp32 values do so once in 2^20, and take the product.
+template <bool EXACT>
+__device__ __forceinline__ float quotient(float x, float inv, float low) {
+    return EXACT ? __builtin_fmaf(x, inv, x * low) : x * inv;
+}
+
 // Quotient where pre is not 1: a scale down there may itself be rounded so
 // coarsely (subnormals) that its largest value is past 448 times it.
-__device__ __forceinline__ float tiny_quotient(float x, float pre, float inv) {
-    const float q = x * pre * inv;
+template <bool EXACT = false>
+__device__ __forceinline__ float tiny_quotient(float x, float pre, float inv, float low = 0.f) {
+    const float q = quotient<EXACT>(x * pre, inv, low);
     return q != q ? q : fminf(fmaxf(q, -448.f), 448.f);
 }
 
 // N values of one group -> their codes, four to a word.
-template <int N>
+template <int N, bool EXACT = false>
 __device__ __forceinline__ void quantize(const float* v, const GroupScale& g, uint32_t* q) {
     if (g.pre == 1.f) {
 #pragma unroll
         for (int i = 0; i < N; i += 4)
-            q[i / 4] = e4m3_x4(v[i] * g.inv, v[i + 1] * g.inv, v[i + 2] * g.inv, v[i + 3] * g.inv);
+            q[i / 4] = e4m3_x4(quotient<EXACT>(v[i], g.inv, g.low), quotient<EXACT>(v[i + 1], g.inv, g.low),
+                               quotient<EXACT>(v[i + 2], g.inv, g.low), quotient<EXACT>(v[i + 3], g.inv, g.low));
     } else {
 #pragma unroll
         for (int i = 0; i < N; i += 4)
-            q[i / 4] = e4m3_x4(tiny_quotient(v[i], g.pre, g.inv), tiny_quotient(v[i + 1], g.pre, g.inv),
-                               tiny_quotient(v[i + 2], g.pre, g.inv), tiny_quotient(v[i + 3], g.pre, g.inv));
+            q[i / 4] = e4m3_x4(tiny_quotient<EXACT>(v[i], g.pre, g.inv, g.low),
+                               tiny_quotient<EXACT>(v[i + 1], g.pre, g.inv, g.low),
+                               tiny_quotient<EXACT>(v[i + 2], g.pre, g.inv, g.low),
+                               tiny_quotient<EXACT>(v[i + 3], g.pre, g.inv, g.low));
     }
 }
 

@@ -25,9 +25,13 @@ static dim3 item_grid(int64_t items) { return run_grid<kItemRun>((items + kThrea
 // Rows outside [0, rows) (no expert, over the capacity) are skipped.
 __device__ __forceinline__ int uniform_row(const int32_t* p) { return __builtin_amdgcn_readfirstlane(*p); }
 
-// Up to 8 bf16 of a row piece: one 16-byte load where all 8 are there.
+// Up to 8 bf16 of a row piece: one 16-byte load where all 8 are there.  Expert
+// rows are streamed (ONCE).  Tokens and their gradients are not: they are small
+// beside them and mostly just written, so that they come from the memory-side
+// cache, which streaming loads do without.
+template <bool ONCE>
 __device__ __forceinline__ u32x4 load8(const uint16_t* p, int n) {
-    if (n >= 8) return __builtin_nontemporal_load((const u32x4_a2*)p);
+    if (n >= 8) return ONCE ? __builtin_nontemporal_load((const u32x4_a2*)p) : *(const u32x4_a2*)p;
     uint32_t v[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 7; ++i)
@@ -54,7 +58,8 @@ __device__ __forceinline__ void unpack8(u32x4 v, float* f) {
 // ----------------------------------------------------------------- dispatch
 
 // bf16: a wave copies 512 elements of a token to its k rows.  4096 tokens of
-// 7168 to 8 experts each: 107 us, 4.9 TB/s of one read and 8 writes.
+// 7168 to 8 experts each: 92 us, 5.7 TB/s of one read and 8 writes (101 us from
+// HBM; 108 us with streamed loads).
 __global__ __launch_bounds__(kThreads) void dispatch_bf16_kernel(PermuteArgs a, int chunks) {
     const int64_t item = wave_item();
     if (item >= (int64_t)a.T * chunks) return;
@@ -62,7 +67,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_bf16_kernel(PermuteArgs a, 
     const int64_t t = item / chunks;
     const int c = (int)(item % chunks) * 512 + lane * 8, n = a.W - c;
     if (n <= 0) return;
-    const u32x4 v = load8((const uint16_t*)a.x + t * a.W + c, n);
+    const u32x4 v = load8<false>((const uint16_t*)a.x + t * a.W + c, n);
     for (int j = 0; j < a.k; ++j) {
         const int row = uniform_row(a.row_of + t * a.k + j);
         if ((uint32_t)row < (uint32_t)a.rows) store8((uint16_t*)a.out + (int64_t)row * a.W + c, v, n);
@@ -70,9 +75,10 @@ __global__ __launch_bounds__(kThreads) void dispatch_bf16_kernel(PermuteArgs a, 
 }
 
 // e4m3: a wave quantizes 1024 elements (8 groups) of a token, 16 a lane, and
-// stores them to its k rows.  The same 4096 tokens: 57 us with row-major scales
-// (5.3 TB/s), 64 us with transposed ones.  Those are 4 bytes to a line each, 1.8
-// million of them; giving an XCD neighbouring tokens or neighbouring columns
+// stores them to its k rows.  The same 4096 tokens: 46 us with row-major scales
+// (6.5 TB/s), 50 us with transposed ones; 54 and 61 us with the tokens from HBM,
+// 57 and 64 us with streamed loads.  Transposed scales are 4 bytes to a line each,
+// 1.8 million of them; giving an XCD neighbouring tokens or neighbouring columns
 // (whole lines then merge in its L2) makes no difference.
 template <OperandFormat FMT>
 __global__ __launch_bounds__(kThreads) void dispatch_fp8_kernel(PermuteArgs a, int chunks) {
@@ -85,8 +91,8 @@ __global__ __launch_bounds__(kThreads) void dispatch_fp8_kernel(PermuteArgs a, i
     u32x4 x0 = {0, 0, 0, 0}, x1 = {0, 0, 0, 0};
     if (in) {
         const u32x4* p = (const u32x4*)((const uint16_t*)a.x + t * a.W + c);
-        x0 = load_once(p);
-        x1 = load_once(p + 1);
+        x0 = p[0];                                       // halves of a line each: a streaming load fetches it twice
+        x1 = p[1];
     }
     float f[16];
     unpack8(x0, f);
@@ -96,7 +102,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_fp8_kernel(PermuteArgs a, i
     for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(f[i]));
     const GroupScale g = group_scale<FMT == kE8m0>(max8(m));
     uint32_t codes[4];
-    quantize<16>(f, g, codes);
+    quantize<16, FMT != kE8m0>(f, g, codes);
     const u32x4 q = {codes[0], codes[1], codes[2], codes[3]};
     const int kg = c / kGroup, groups = a.W / kGroup;
     for (int j0 = 0; j0 < a.k; j0 += 8) {
@@ -142,7 +148,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(PermuteArgs a, int ch
             const int row = __builtin_amdgcn_readlane(srow, j);
             v[j] = u32x4{0, 0, 0, 0};
             if ((uint32_t)row < (uint32_t)a.rows && n > 0)
-                v[j] = load8((const uint16_t*)a.x + (int64_t)row * a.W + c, n);
+                v[j] = load8<true>((const uint16_t*)a.x + (int64_t)row * a.W + c, n);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -165,10 +171,13 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(PermuteArgs a, int ch
 // A workgroup takes a token: dY rows are weight * dout, and each weight's
 // gradient is the dot product of its row of Y with dout, summed in fp32 in a
 // fixed order (lane pieces, wave, waves).  dout is read once per 8 rows.  32768
-// rows of 7168 in bf16: 189 us, 5.3 TB/s, and 158 us with e4m3 dY; as many
+// rows of 7168 in bf16: 182 us, 5.5 TB/s, and 143 us with e4m3 dY; as many
 // waves as there are 512-column pieces, since 4 waves going round take 202 us.
 template <OperandFormat FMT>
 __global__ __launch_bounds__(1024) void combine_backward_kernel(PermuteArgs a) {
+    // Rows loaded at a time.  With quantization beside them, 8 leave one workgroup a CU at 7168 columns (158 us), 2
+    // leave two (144 us); in bf16 there are two either way.
+    constexpr int kAhead = FMT == kBf16 ? 8 : 2;
     __shared__ float part_s[16][8];
     const int64_t t = blockIdx.x;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -182,15 +191,8 @@ __global__ __launch_bounds__(1024) void combine_backward_kernel(PermuteArgs a) {
         for (int j = 0; j < 8; ++j) dot[j] = 0.f;
         for (int c0 = wave * 512; c0 < a.W; c0 += (int)blockDim.x * 8) {
             const int c = c0 + lane * 8, n = a.W - c;
-            u32x4 y[8], dv = {0, 0, 0, 0};
-            if (n > 0) dv = load8((const uint16_t*)a.x + t * a.W + c, n);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int row = __builtin_amdgcn_readlane(srow, j);
-                y[j] = u32x4{0, 0, 0, 0};
-                if ((uint32_t)row < (uint32_t)a.rows && n > 0)
-                    y[j] = load8((const uint16_t*)a.Y + (int64_t)row * a.W + c, n);
-            }
+            u32x4 dv = {0, 0, 0, 0};
+            if (n > 0) dv = load8<false>((const uint16_t*)a.x + t * a.W + c, n);
             float d[8];
             unpack8(dv, d);
             float amax = 0.f;
@@ -200,38 +202,50 @@ __global__ __launch_bounds__(1024) void combine_backward_kernel(PermuteArgs a) {
                 amax = max16(amax);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int row = __builtin_amdgcn_readlane(srow, j);
-                if ((uint32_t)row >= (uint32_t)a.rows) continue;
-                const float w = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(sw), j));
-                float f[8], o[8];
-                unpack8(y[j], f);
+            for (int h = 0; h < 8; h += kAhead) {
+                u32x4 y[kAhead];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    dot[j] = __builtin_fmaf(f[i], d[i], dot[j]);
-                    o[i] = w * d[i];
+                for (int j = h; j < h + kAhead; ++j) {
+                    const int row = __builtin_amdgcn_readlane(srow, j);
+                    y[j - h] = u32x4{0, 0, 0, 0};
+                    if ((uint32_t)row < (uint32_t)a.rows && n > 0)
+                        y[j - h] = load8<true>((const uint16_t*)a.Y + (int64_t)row * a.W + c, n);
                 }
-                if (FMT == kBf16) {
-                    u32x4 v;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
-                    if (n > 0) store8((uint16_t*)a.out + (int64_t)row * a.W + c, v, n);
-                } else {
-                    // rounding keeps order: the largest |w d| is |w| times the largest |d|, rounded
-                    const GroupScale g = group_scale<FMT == kE8m0>(fabsf(w * amax));
-                    uint32_t codes[2];
-                    quantize<8>(o, g, codes);
-                    const u32x2 q = {codes[0], codes[1]};
-                    if (n > 0) {
-                        store_once((uint8_t*)a.out + (int64_t)row * a.W + c, q);
-                        if ((lane & 15) == 0) {
-                            const int kg = c / kGroup;
-                            if (FMT == kRows) ((float*)a.scale)[(int64_t)row * groups + kg] = g.s;
-                            if (FMT == kKm) ((float*)a.scale)[(int64_t)kg * a.rows + row] = g.s;
-                            if (FMT == kE8m0) ((uint8_t*)a.scale)[(int64_t)kg * a.rows + row] = (uint8_t)g.byte;
+                for (int j = h; j < h + kAhead; ++j) {
+                    const int row = __builtin_amdgcn_readlane(srow, j);
+                    if ((uint32_t)row >= (uint32_t)a.rows) continue;
+                    const float w = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(sw), j));
+                    float f[8], o[8];
+                    unpack8(y[j - h], f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        dot[j] = __builtin_fmaf(f[i], d[i], dot[j]);
+                        o[i] = w * d[i];
+                    }
+                    if (FMT == kBf16) {
+                        u32x4 v;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
+                        if (n > 0) store8((uint16_t*)a.out + (int64_t)row * a.W + c, v, n);
+                    } else {
+                        // rounding keeps order: the largest |w d| is |w| times the largest |d|, rounded
+                        const GroupScale g = group_scale<FMT == kE8m0>(fabsf(w * amax));
+                        uint32_t codes[2];
+                        quantize<8>(o, g, codes);
+                        const u32x2 q = {codes[0], codes[1]};
+                        if (n > 0) {
+                            store_once((uint8_t*)a.out + (int64_t)row * a.W + c, q);
+                            if ((lane & 15) == 0) {
+                                const int kg = c / kGroup;
+                                if (FMT == kRows) ((float*)a.scale)[(int64_t)row * groups + kg] = g.s;
+                                if (FMT == kKm) ((float*)a.scale)[(int64_t)kg * a.rows + row] = g.s;
+                                if (FMT == kE8m0) ((uint8_t*)a.scale)[(int64_t)kg * a.rows + row] = (uint8_t)g.byte;
+                            }
                         }
                     }
                 }
+                __builtin_amdgcn_sched_barrier(0);       // the next rows' loads not before: their registers
             }
         }
 #pragma unroll

@@ -367,6 +367,24 @@ def test_dispatch_and_combine_odd_widths(K):
     assert (np.abs(f64(dw) - rw) <= (8 * -(-K // 2048) + 24) * U * magw).all()
 
 
+@pytest.mark.parametrize("fmt", ["rows", "km"])
+def test_dispatch_codes_on_rounding_borders(fmt):
+    """bf16 values over a bf16 maximum lie on e4m3's borders once in two hundred: codes are those of the fp32 quotient."""
+    T, K, k = 64, 1024, 2
+    x = torch.randn(T, K, generator=gen(21)).to(BF16)
+    g = x.float().reshape(T, -1, 128)
+    s = g.abs().amax(-1) / 448
+    q = g / s[..., None]
+    ratio = g.double() / s.double()[..., None]
+    near = torch.frexp(ratio)[0].abs() * 16 % 1            # a border has 4 bits after the leading one, the last set
+    assert ((near - 0.5).abs() < 2.0 ** -19).sum() > 200   # there are such values here
+    A, sc = operand((T * k,), T * k, K, fmt)
+    mg.dispatch(x.cuda(), torch.arange(T * k, dtype=torch.int32).view(T, k).cuda(), A, sc, scale_km=fmt == "km")
+    want = q.clamp(-448, 448).to(E4M3).reshape(T, K).view(torch.uint8).repeat_interleave(k, 0)
+    assert torch.equal(A.cpu().view(torch.uint8), want)
+    assert torch.equal((sc.t() if fmt == "km" else sc).cpu(), s.repeat_interleave(k, 0))
+
+
 def test_dispatch_special_values():
     K = 512
     x = torch.randn(2, K, generator=gen(2)).to(BF16)
