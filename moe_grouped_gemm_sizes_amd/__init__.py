@@ -595,13 +595,31 @@ def route_workspace(T: int, E: int, device="cuda") -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _top_k(t, name: str, T: int) -> int:
-    """k of an int32 [T, k] tensor."""
-    if isinstance(t, torch.Tensor) and t.dim() == 2:
-        k = t.shape[1]
-        _need(t, name, (T, k), (torch.int32,))
-        return k
-    _need(t, name, (T, None), (torch.int32,))
+_ABSENT = (None, "", None, None)                             # an optional tensor that was not given
+
+
+def _pointers(*specs):
+    """Data pointers of (tensor, name, shape, dtype) specs; None for _ABSENT.  One pass where each is a contiguous
+    tensor as specified on one GPU; else the checks one by one, for their messages."""
+    out = []
+    try:
+        dev = specs[0][0].get_device()
+        for t, _, shape, dtype in specs:
+            if shape is None:
+                out.append(None)
+            elif t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+                out.append(t.data_ptr())
+            else:
+                break
+    except AttributeError:                                   # not a tensor
+        dev = -1
+    if dev >= 0 and len(out) == len(specs):
+        return out
+    for t, name, shape, dtype in specs:
+        if shape is not None:
+            _need(t, name, shape, (dtype,))
+    _one_device(*(s[0] for s in specs))
+    return [_p(s[0]) for s in specs]
 
 
 def _matrix(t, name: str, dtypes):
@@ -611,9 +629,7 @@ def _matrix(t, name: str, dtypes):
     return t.shape
 
 
-def _logits(logits) -> Tuple[int, int, int]:
-    T, E = _matrix(logits, "logits", (torch.float32, torch.bfloat16))
-    return T, E, LOGITS_BF16 if logits.dtype == torch.bfloat16 else LOGITS_FP32
+_F, _H, _I = torch.float32, torch.bfloat16, torch.int32
 
 
 def route(logits, ids, weights, m_sizes, row_of, ws, *, rows_total: int, bias=None, score: int = SCORE_SOFTMAX,
@@ -623,103 +639,104 @@ def route(logits, ids, weights, m_sizes, row_of, ws, *, rows_total: int, bias=No
     sigmoid score (plus bias [E] for the choice alone), group-limited when n_groups > 1; row_of is the row of every
     assignment in the contiguous layout of rows_total rows, or with cap > 0 in [E, cap] capacity buffers
     (rows_total = E * cap); -1 where there is none.  ws: route_workspace(T, E)."""
-    T, E, kind = _logits(logits)
-    k = _top_k(ids, "ids", T)
-    _need(weights, "weights", (T, k), (torch.float32,))
-    _need(m_sizes, "m_sizes", (E,), (torch.int32,))
-    _need(row_of, "row_of", (T, k), (torch.int32,))
-    if bias is not None:
-        _need(bias, "bias", (E,), (torch.float32,))
-    _need(ws, "ws", (None,), (torch.uint8,))
+    T, E = _matrix(logits, "logits", (_F, _H))
+    k = _matrix(ids, "ids", (_I,))[1]
+    kind = logits.dtype
+    n = ws.numel() if isinstance(ws, torch.Tensor) else 0
     need = route_workspace_bytes(T, E)
-    if ws.numel() < need:
-        raise ValueError(f"ws: {ws.numel()} bytes, need {need} (route_workspace_bytes({T}, {E}))")
-    _one_device(logits, ids, weights, m_sizes, row_of, bias, ws)
-    _check(lib().moegg_route(_p(logits), kind, _p(bias), _p(ids), _p(weights), _p(m_sizes), _p(row_of), T, E, k,
-                             score, n_groups, topk_groups, group_top, renorm, scale, rows_total, seg_align, cap,
-                             _p(ws), ws.numel(), _stream(stream)), "moegg_route")
+    if n < need:
+        raise ValueError(f"ws: {n} bytes, need {need} (route_workspace_bytes({T}, {E}))")
+    l, i, w, m, r, b, s = _pointers(
+        (logits, "logits", (T, E), kind), (ids, "ids", (T, k), _I), (weights, "weights", (T, k), _F),
+        (m_sizes, "m_sizes", (E,), _I), (row_of, "row_of", (T, k), _I), (bias, "bias", (E,), _F) if bias is not None else _ABSENT,
+        (ws, "ws", (n,), torch.uint8))
+    _check(lib().moegg_route(l, LOGITS_BF16 if kind is _H else LOGITS_FP32, b, i, w, m, r, T, E, k, score, n_groups,
+                             topk_groups, group_top, renorm, scale, rows_total, seg_align, cap, s, n,
+                             _stream(stream)), "moegg_route")
 
 
 def route_backward(logits, ids, d_weights, d_logits, *, score: int = SCORE_SOFTMAX, renorm: bool = True,
                    scale: float = 1.0, stream=None):
     """d_logits [T, E] (logits' dtype) from d_weights [T, k] and the ids that route chose (see moegg.h)."""
-    T, E, kind = _logits(logits)
-    k = _top_k(ids, "ids", T)
-    _need(d_weights, "d_weights", (T, k), (torch.float32,))
-    _need(d_logits, "d_logits", [T, E], (logits.dtype,))
-    _one_device(logits, ids, d_weights, d_logits)
-    _check(lib().moegg_route_backward(_p(logits), kind, _p(ids), _p(d_weights), _p(d_logits), T, E, k, score, renorm,
+    T, E = _matrix(logits, "logits", (_F, _H))
+    k = _matrix(ids, "ids", (_I,))[1]
+    kind = logits.dtype
+    l, i, dw, dl = _pointers((logits, "logits", (T, E), kind), (ids, "ids", (T, k), _I),
+                             (d_weights, "d_weights", (T, k), _F), (d_logits, "d_logits", (T, E), kind))
+    _check(lib().moegg_route_backward(l, LOGITS_BF16 if kind is _H else LOGITS_FP32, i, dw, dl, T, E, k, score, renorm,
                                       scale, _stream(stream)), "moegg_route_backward")
 
 
-def _row_operand(A, name: str, A_scale, width: int, scale_km: bool) -> Tuple[int, int]:
-    """Rows and operand type code of an expert-side operand [rows, width] or [G, cap, width] and its scales."""
+def _row_operand(A, name: str, A_scale, width: int, scale_km: bool):
+    """Rows and operand type code of an expert-side operand [rows, width] or [G, cap, width], and the specs of it and
+    its scales."""
     if not isinstance(A, torch.Tensor) or A.dim() not in (2, 3):
         raise ValueError(f"{name}: tensor [rows, width] or [G, cap, width] expected")
-    _need(A, name, (*A.shape[:-1], width), (torch.bfloat16, _E4M3))
-    rows = A.shape[0] if A.dim() == 2 else A.shape[0] * A.shape[1]
-    if A.dtype == torch.bfloat16:
+    kind, lead = A.dtype, A.shape[:-1]
+    rows = lead[0] if len(lead) == 1 else lead[0] * lead[1]
+    spec = (A, name, lead + (width,), kind)
+    if kind is _H:
         _none(A_scale, f"{name}_scale", "for a bf16 operand")
         if scale_km:
             raise ValueError("scale_km applies to e4m3 operands with fp32 scales")
-        return rows, BF16
+        return rows, BF16, spec, _ABSENT
+    if kind is not _E4M3:
+        _need(A, name, lead + (width,), (_H, _E4M3))
     if width % 128:
         raise ValueError(f"{name}: width {width}, e4m3 operands need a multiple of 128")
-    if isinstance(A_scale, torch.Tensor) and A_scale.dtype == torch.uint8:
+    groups = width // 128
+    if isinstance(A_scale, torch.Tensor) and A_scale.dtype is torch.uint8:
         if scale_km:
             raise ValueError("scale_km applies to e4m3 operands with fp32 scales")
-        _need(A_scale, f"{name}_scale", (width // 128, rows), (torch.uint8,))
-        return rows, FP8_E4M3_E8M0
-    _need(A_scale, f"{name}_scale", [width // 128, rows] if scale_km else [*A.shape[:-1], width // 128],
-          (torch.float32,))
-    return rows, FP8_E4M3_SCALE_KM if scale_km else FP8_E4M3
+        return rows, FP8_E4M3_E8M0, spec, (A_scale, f"{name}_scale", (groups, rows), torch.uint8)
+    return (rows, FP8_E4M3_SCALE_KM if scale_km else FP8_E4M3, spec,
+            (A_scale, f"{name}_scale", (groups, rows) if scale_km else lead + (groups,), _F))
 
 
 def dispatch(x, row_of, A, A_scale=None, *, scale_km: bool = False, stream=None):
     """A[row_of[t, j]] = x[t] (see moegg.h).  x bf16 [T, K]; A bf16 or e4m3, [rows, K] or [G, cap, K], with the
     scales of the grouped GEMM that reads it: fp32 [rows, K/128] ([G, cap, K/128]), [K/128, rows] (scale_km), or
     uint8 E8M0 bytes [K/128, rows]."""
-    T, K = _matrix(x, "x", (torch.bfloat16,))
-    k = _top_k(row_of, "row_of", T)
-    rows, code = _row_operand(A, "A", A_scale, K, scale_km)
-    _one_device(x, row_of, A, A_scale)
-    _check(lib().moegg_dispatch(_p(x), _p(row_of), _p(A), _p(A_scale), T, k, K, rows, code,
-                                _stream(stream)), "moegg_dispatch")
+    T, K = _matrix(x, "x", (_H,))
+    k = _matrix(row_of, "row_of", (_I,))[1]
+    rows, code, spec, spec_scale = _row_operand(A, "A", A_scale, K, scale_km)
+    px, pr, pa, ps = _pointers((x, "x", (T, K), _H), (row_of, "row_of", (T, k), _I), spec, spec_scale)
+    _check(lib().moegg_dispatch(px, pr, pa, ps, T, k, K, rows, code, _stream(stream)), "moegg_dispatch")
 
 
-def _expert_rows(Y, N: int) -> int:
+def _expert_rows(Y, N: int):
+    """Rows of bf16 Y [rows, N] or [G, cap, N], and its spec."""
     if not isinstance(Y, torch.Tensor) or Y.dim() not in (2, 3):
         raise ValueError("Y: tensor [rows, N] or [G, cap, N] expected")
-    _need(Y, "Y", (*Y.shape[:-1], N), (torch.bfloat16,))
-    return Y.shape[0] if Y.dim() == 2 else Y.shape[0] * Y.shape[1]
+    lead = Y.shape[:-1]
+    return lead[0] if len(lead) == 1 else lead[0] * lead[1], (Y, "Y", lead + (N,), _H)
 
 
 def combine(Y, row_of, out, weights=None, *, stream=None):
     """out[t] = sum_j weights[t, j] * Y[row_of[t, j]] (see moegg.h); weights None: all 1, which is also dispatch's
     backward pass.  Y bf16 [rows, N] or [G, cap, N], out bf16 [T, N], weights fp32 [T, k]."""
-    T, N = _matrix(out, "out", (torch.bfloat16,))
-    k = _top_k(row_of, "row_of", T)
-    rows = _expert_rows(Y, N)
-    if weights is not None:
-        _need(weights, "weights", (T, k), (torch.float32,))
-    _one_device(Y, row_of, out, weights)
-    _check(lib().moegg_combine(_p(Y), _p(row_of), _p(weights), _p(out), T, k, N, rows,
-                               _stream(stream)), "moegg_combine")
+    T, N = _matrix(out, "out", (_H,))
+    k = _matrix(row_of, "row_of", (_I,))[1]
+    rows, spec = _expert_rows(Y, N)
+    py, pr, po, pw = _pointers(spec, (row_of, "row_of", (T, k), _I), (out, "out", (T, N), _H),
+                               (weights, "weights", (T, k), _F) if weights is not None else _ABSENT)
+    _check(lib().moegg_combine(py, pr, pw, po, T, k, N, rows, _stream(stream)), "moegg_combine")
 
 
 def combine_backward(dout, Y, weights, row_of, dY, d_weights, dY_scale=None, *, scale_km: bool = False, stream=None):
     """dY[row_of[t, j]] = weights[t, j] * dout[t] in dY's operand format (as dispatch's A), and d_weights[t, j] =
     <Y[row_of[t, j]], dout[t]> (see moegg.h)."""
-    T, N = _matrix(dout, "dout", (torch.bfloat16,))
-    k = _top_k(row_of, "row_of", T)
-    _need(weights, "weights", (T, k), (torch.float32,))
-    _need(d_weights, "d_weights", (T, k), (torch.float32,))
-    rows, code = _row_operand(dY, "dY", dY_scale, N, scale_km)
-    if _expert_rows(Y, N) != rows:
+    T, N = _matrix(dout, "dout", (_H,))
+    k = _matrix(row_of, "row_of", (_I,))[1]
+    rows, code, spec, spec_scale = _row_operand(dY, "dY", dY_scale, N, scale_km)
+    y_rows, y_spec = _expert_rows(Y, N)
+    if y_rows != rows:
         raise ValueError(f"Y: shape {list(Y.shape)}, expected {rows} rows as dY")
-    _one_device(dout, Y, weights, row_of, dY, d_weights, dY_scale)
-    _check(lib().moegg_combine_backward(_p(dout), _p(Y), _p(weights), _p(row_of), _p(dY), _p(dY_scale), _p(d_weights),
-                                        T, k, N, rows, code, _stream(stream)), "moegg_combine_backward")
+    pd, py, pw, pr, pg, ps, pdw = _pointers(
+        (dout, "dout", (T, N), _H), y_spec, (weights, "weights", (T, k), _F), (row_of, "row_of", (T, k), _I), spec,
+        spec_scale, (d_weights, "d_weights", (T, k), _F))
+    _check(lib().moegg_combine_backward(pd, py, pw, pr, pg, ps, pdw, T, k, N, rows, code, _stream(stream)),
+           "moegg_combine_backward")
 
 
 def _no_e8m0(code: int, name: str):
@@ -727,38 +744,41 @@ def _no_e8m0(code: int, name: str):
         raise ValueError(f"{name}: fp32 scales expected")
 
 
-def _token_group_scales(X_scale, name: str, width: int, groups: Optional[int] = None, dtype=None) -> int:
-    _need(X_scale, name, (groups, width), (torch.float32, torch.uint8) if dtype is None else (dtype,))
-    return X_scale.shape[0]
+def _token_group_scales(X_scale, name: str) -> int:
+    return _matrix(X_scale, name, (_F, torch.uint8))[0]
+
+
+def _counts_spec(m_sizes):
+    """The number of experts, and m_sizes' spec."""
+    if not isinstance(m_sizes, torch.Tensor) or m_sizes.dim() != 1 or m_sizes.shape[0] < 1:
+        _counts(m_sizes, "m_sizes")
+    G = m_sizes.shape[0]
+    return G, (m_sizes, "m_sizes", (G,), _I)
 
 
 def swiglu_checkpoint(GU, m_sizes, H, ckpt, ckpt_scale, H_scale=None, *, scale_km: bool = False, stream=None):
     """H = silu(g) * u of GU bf16 [rows, 2I] (columns in interleave_gate_up's order), and GU kept as e4m3 ckpt
     [rows, 2I] with fp32 ckpt_scale [rows, 2I/128] (see moegg.h).  H bf16 [rows, I], or e4m3 with H_scale fp32
     [rows, I/128] ([I/128, rows] with scale_km)."""
-    rows, I = _matrix(H, "H", (torch.bfloat16, _E4M3))
-    _, code = _row_operand(H, "H", H_scale, I, scale_km)
+    rows, I = _matrix(H, "H", (_H, _E4M3))
+    _, code, spec, spec_scale = _row_operand(H, "H", H_scale, I, scale_km)
     _no_e8m0(code, "H_scale")
-    _need(GU, "GU", (rows, 2 * I), (torch.bfloat16,))
-    _need(ckpt, "ckpt", (rows, 2 * I), (_E4M3,))
-    _need(ckpt_scale, "ckpt_scale", (rows, 2 * I // 128), (torch.float32,))
-    _counts(m_sizes, "m_sizes")
-    _one_device(GU, m_sizes, H, ckpt, ckpt_scale, H_scale)
-    _check(lib().moegg_swiglu_checkpoint(_p(GU), _p(m_sizes), _p(H), _p(H_scale), _p(ckpt), _p(ckpt_scale),
-                                         m_sizes.numel(), rows, I, code, _stream(stream)), "moegg_swiglu_checkpoint")
+    G, counts = _counts_spec(m_sizes)
+    pg, pm, ph, phs, pc, pcs = _pointers(
+        (GU, "GU", (rows, 2 * I), _H), counts, spec, spec_scale, (ckpt, "ckpt", (rows, 2 * I), _E4M3),
+        (ckpt_scale, "ckpt_scale", (rows, 2 * I // 128), _F))
+    _check(lib().moegg_swiglu_checkpoint(pg, pm, ph, phs, pc, pcs, G, rows, I, code, _stream(stream)),
+           "moegg_swiglu_checkpoint")
 
 
 def swiglu_checkpoint_backward(dH, m_sizes, ckpt, ckpt_scale, dGU, H, *, stream=None):
     """dGU bf16 [rows, 2I] and H bf16 [rows, I] again, from dH bf16 [rows, I] and the checkpoint (see moegg.h)."""
-    rows, I = _matrix(dH, "dH", (torch.bfloat16,))
-    _need(ckpt, "ckpt", (rows, 2 * I), (_E4M3,))
-    _need(ckpt_scale, "ckpt_scale", (rows, 2 * I // 128), (torch.float32,))
-    _need(dGU, "dGU", (rows, 2 * I), (torch.bfloat16,))
-    _need(H, "H", (rows, I), (torch.bfloat16,))
-    _counts(m_sizes, "m_sizes")
-    _one_device(dH, m_sizes, ckpt, ckpt_scale, dGU, H)
-    _check(lib().moegg_swiglu_checkpoint_backward(_p(dH), _p(m_sizes), _p(ckpt), _p(ckpt_scale), _p(dGU), _p(H),
-                                                  m_sizes.numel(), rows, I, _stream(stream)),
+    rows, I = _matrix(dH, "dH", (_H,))
+    G, counts = _counts_spec(m_sizes)
+    pd, pm, pc, pcs, pg, ph = _pointers(
+        (dH, "dH", (rows, I), _H), counts, (ckpt, "ckpt", (rows, 2 * I), _E4M3),
+        (ckpt_scale, "ckpt_scale", (rows, 2 * I // 128), _F), (dGU, "dGU", (rows, 2 * I), _H), (H, "H", (rows, I), _H))
+    _check(lib().moegg_swiglu_checkpoint_backward(pd, pm, pc, pcs, pg, ph, G, rows, I, _stream(stream)),
            "moegg_swiglu_checkpoint_backward")
 
 
@@ -767,36 +787,34 @@ def swiglu_checkpoint_backward_fp8(dH, m_sizes, ckpt, ckpt_scale, dGU, dGU_scale
     """The operands of both gradients' products from dH bf16 [rows, I] and the checkpoint (see moegg.h): dGU e4m3
     [rows, 2I] with fp32 dGU_scale [rows, 2I/128] ([2I/128, rows] with scale_km); dGU_k e4m3 [rows, 2I] and H_k
     e4m3 [rows, I] with scales per token group, [S, 2I] and [S, I], fp32 or uint8 E8M0 bytes (k_scale_groups)."""
-    rows, I = _matrix(dH, "dH", (torch.bfloat16,))
-    _need(ckpt, "ckpt", (rows, 2 * I), (_E4M3,))
-    _need(ckpt_scale, "ckpt_scale", (rows, 2 * I // 128), (torch.float32,))
+    rows, I = _matrix(dH, "dH", (_H,))
     _need(dGU, "dGU", (rows, 2 * I), (_E4M3,))
-    _, code = _row_operand(dGU, "dGU", dGU_scale, 2 * I, scale_km)
+    _, code, spec, spec_scale = _row_operand(dGU, "dGU", dGU_scale, 2 * I, scale_km)
     _no_e8m0(code, "dGU_scale")
-    _need(dGU_k, "dGU_k", (rows, 2 * I), (_E4M3,))
-    _need(H_k, "H_k", (rows, I), (_E4M3,))
-    S = _token_group_scales(dGU_k_scale, "dGU_k_scale", 2 * I)
-    _token_group_scales(H_k_scale, "H_k_scale", I, S, dGU_k_scale.dtype)
-    _counts(m_sizes, "m_sizes")
-    _one_device(dH, m_sizes, ckpt, ckpt_scale, dGU, dGU_scale, dGU_k, dGU_k_scale, H_k, H_k_scale)
-    _check(lib().moegg_swiglu_checkpoint_backward_fp8(
-        _p(dH), _p(m_sizes), _p(ckpt), _p(ckpt_scale), _p(dGU), _p(dGU_scale), _p(dGU_k), _p(dGU_k_scale), _p(H_k),
-        _p(H_k_scale), m_sizes.numel(), rows, I, S, code, dGU_k_scale.dtype == torch.uint8, _stream(stream)),
-        "moegg_swiglu_checkpoint_backward_fp8")
+    G, counts = _counts_spec(m_sizes)
+    S = _token_group_scales(dGU_k_scale, "dGU_k_scale")
+    kind = dGU_k_scale.dtype
+    p = _pointers(
+        (dH, "dH", (rows, I), _H), counts, (ckpt, "ckpt", (rows, 2 * I), _E4M3),
+        (ckpt_scale, "ckpt_scale", (rows, 2 * I // 128), _F), spec, spec_scale,
+        (dGU_k, "dGU_k", (rows, 2 * I), _E4M3), (dGU_k_scale, "dGU_k_scale", (S, 2 * I), kind),
+        (H_k, "H_k", (rows, I), _E4M3), (H_k_scale, "H_k_scale", (S, I), kind))
+    _check(lib().moegg_swiglu_checkpoint_backward_fp8(*p, G, rows, I, S, code, kind is torch.uint8, _stream(stream)),
+           "moegg_swiglu_checkpoint_backward_fp8")
 
 
 def checkpoint_to_k_groups(X, m_sizes, X_k, X_k_scale, X_scale=None, *, scale_km: bool = False, stream=None):
     """A saved activation X [rows, M] (bf16, or e4m3 with fp32 scales [rows, M/128], [M/128, rows] with scale_km) as
     an operand of grouped_gemm_k_grouped: X_k e4m3 [rows, M] with X_k_scale [S, M], fp32 or uint8 E8M0 (see moegg.h)."""
-    rows, M = _matrix(X, "X", (torch.bfloat16, _E4M3))
-    _, code = _row_operand(X, "X", X_scale, M, scale_km)
+    rows, M = _matrix(X, "X", (_H, _E4M3))
+    _, code, spec, spec_scale = _row_operand(X, "X", X_scale, M, scale_km)
     _no_e8m0(code, "X_scale")
-    _need(X_k, "X_k", (rows, M), (_E4M3,))
-    S = _token_group_scales(X_k_scale, "X_k_scale", M)
-    _counts(m_sizes, "m_sizes")
-    _one_device(X, X_scale, m_sizes, X_k, X_k_scale)
-    _check(lib().moegg_checkpoint_to_k_groups(_p(X), _p(X_scale), _p(m_sizes), _p(X_k), _p(X_k_scale),
-                                              m_sizes.numel(), rows, M, S, code, X_k_scale.dtype == torch.uint8,
+    G, counts = _counts_spec(m_sizes)
+    S = _token_group_scales(X_k_scale, "X_k_scale")
+    kind = X_k_scale.dtype
+    px, ps, pm, pk, pks = _pointers(spec, spec_scale, counts, (X_k, "X_k", (rows, M), _E4M3),
+                                    (X_k_scale, "X_k_scale", (S, M), kind))
+    _check(lib().moegg_checkpoint_to_k_groups(px, ps, pm, pk, pks, G, rows, M, S, code, kind is torch.uint8,
                                               _stream(stream)), "moegg_checkpoint_to_k_groups")
 
 
