@@ -292,15 +292,19 @@ __device__ __forceinline__ void quantize_columns(const float* v, const float* pr
 // LDS), so that the checkpoint and dH are read and SwiGLU is evaluated once.
 // Rows past the group are out of their buffers' range: they read as 0 and
 // their stores are dropped.
-// 32768 rows of 4096 columns: 123 us, 5.0 TB/s, with the VALU busy for two
+// 32768 rows of 4096 columns: 114 us, 5.4 TB/s, with the VALU busy for two
 // thirds of that.  148 registers hold three workgroups a CU.  What counts besides
-// is where the chip works at one time: runs of 2, 16 and 64 neighbouring units to
-// an XCD take 139, 123 and 129 us, cached instead of streaming accesses 132 us.
+// is where the chip works at one time: runs of 2, 16, 17 and 64 neighbouring units
+// to an XCD take 139, 121, 114 and 129 us (odd runs of 11 to 21 are alike, even ones
+// put the XCDs at equal distances in powers of two), cached instead of streaming
+// accesses 132 us.  Only H_k's stores are cached: a unit writes half lines of it,
+// which meet their other halves in L2 (streamed: 3 us more).
 // Earlier forms: SwiGLU evaluated again for the columns, in 121 registers, 166 us
 // (the VALU was the limit); 256 columns and 512 threads 187 us (one workgroup a
-// CU); workgroups that go on to further tiles and load them ahead 167 us.
+// CU); 512 threads of half the registers 135 us; workgroups that go on to further
+// tiles and load them ahead 167 us.
 constexpr int kBwdCols = 128, kBwdRows = kThreads / 8, kBwdPasses = 128 / kBwdRows;
-constexpr int kBwdRun = 16;
+constexpr int kBwdRun = 17;
 
 template <bool ONCE = true>
 __device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t soff) {
@@ -411,8 +415,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_fp8_kernel(Checkpoin
         const uint32_t step = (uint32_t)(p * kBwdRows * upr);
         __builtin_amdgcn_raw_buffer_store_b128(join_codes(u32x2{q[0], q[1]}, u32x2{q[2], q[3]}, odd), k_out,
                                                (int)(at * kBwdCols + l8 * 16), (int)(step * kBwdCols), CP_NT);
-        __builtin_amdgcn_raw_buffer_store_b64(u32x2{qh[0], qh[1]}, hk_out, (int)(at * 64 + l8 * 8), (int)(step * 64),
-                                              CP_NT);
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{qh[0], qh[1]}, hk_out, (int)(at * 64 + l8 * 8), (int)(step * 64), 0);
     }
 }
 
@@ -421,10 +424,12 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_fp8_kernel(Checkpoin
 // A workgroup takes a token group x 256 columns: 4 waves, 16 rows at a time, 8
 // times.  The codes (or bf16 values) stay in registers as they were read, and
 // are scaled twice: for the columns' maxima and for the new codes.  32768 rows of
-// 7168 columns: 89 us, 5.4 TB/s (cached accesses: 94 us; values kept in fp32
-// between the two: 100 us).  bf16 loads are not streamed: each takes the halves of
-// lines, which would then be fetched twice (4096 columns: 75 us, 82 us streamed).
-constexpr int kKgRows = kThreads / 16, kKgPasses = 128 / kKgRows, kKgRun = 8;
+// 7168 columns: 85 us, 5.7 TB/s, in runs of 11 units to an XCD (of 8: 89 us, of 16:
+// 90 us; odd runs from 3 to 13 within 2 us).  In runs of 8, cached accesses took
+// 94 us and values kept in fp32 between the two 100 us.  bf16 loads are not
+// streamed: each takes the halves of lines, which would then be fetched twice (4096
+// columns: 75 us, 82 us streamed).
+constexpr int kKgRows = kThreads / 16, kKgPasses = 128 / kKgRows, kKgRun = 11;
 
 template <OperandFormat FMT, bool E8M0>
 __global__ __launch_bounds__(kThreads) void k_groups_kernel(CheckpointArgs a) {
