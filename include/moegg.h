@@ -573,7 +573,7 @@ typedef enum {
     MOEGG_SCORE_SIGMOID = 1      /* 1 / (1 + e^-x), each expert by itself */
 } moegg_score_t;
 
-/* Workspace bytes of moegg_route for T tokens and E experts.  Pure host
+/* Workspace bytes of moegg_route for up to T tokens and up to E experts.  Pure host
  * function.  Returns 0 for invalid arguments. */
 size_t moegg_route_workspace_bytes(int T, int E);
 

@@ -583,7 +583,7 @@ def grouped_gemm_k_grouped(X, dY, dW, t_sizes, ws, X_scale=None, dY_scale=None, 
 # ---------------------------------------------------------------- the layer around the grouped GEMMs
 
 
-@functools.lru_cache(maxsize=64)
+@functools.lru_cache(maxsize=4096)
 def route_workspace_bytes(T: int, E: int) -> int:
     return int(lib().moegg_route_workspace_bytes(T, E))
 
@@ -638,7 +638,7 @@ def route(logits, ids, weights, m_sizes, row_of, ws, *, rows_total: int, bias=No
     """logits [T, E] -> ids, weights, row_of [T, k] and m_sizes [E] (see moegg.h): top-k experts by softmax or
     sigmoid score (plus bias [E] for the choice alone), group-limited when n_groups > 1; row_of is the row of every
     assignment in the contiguous layout of rows_total rows, or with cap > 0 in [E, cap] capacity buffers
-    (rows_total = E * cap); -1 where there is none.  ws: route_workspace(T, E)."""
+    (rows_total = E * cap); -1 where there is none.  ws: route_workspace(T, E), or of more tokens or experts."""
     T, E = _matrix(logits, "logits", (_F, _H))
     k = _matrix(ids, "ids", (_I,))[1]
     kind = logits.dtype

@@ -109,7 +109,7 @@ extern "C" {
 
 size_t moegg_route_workspace_bytes(int T, int E) {
     if (T < 0 || T > kRouteMaxTokens || E < 1 || E > kRouteMaxExperts) return 0;
-    const size_t tiles = ((size_t)T + route_tile_tokens(T) - 1) / route_tile_tokens(T);
+    const size_t tiles = std::min<size_t>(((size_t)T + 3) / 4, kRouteMaxTiles);   // of any call of up to T tokens
     return align256(std::max<size_t>(tiles, 1) * sizeof(uint16_t) * (size_t)route_count_width(E));
 }
 

@@ -47,7 +47,10 @@ def test_route_workspace_bytes():
     assert f(-1, 8) == f(8, 0) == f(8, 1025) == f(1 << 30, 8) == 0
     assert f(0, 8) > 0 and f(1, 1) % 256 == 0
     assert f(4096, 64) == 256 * 64 * 2                     # 256 tiles of 16 tokens, 16-bit counts
-    assert f(4097, 63) == 129 * 64 * 2 // 256 * 256 + (256 if 129 * 64 * 2 % 256 else 0)   # tiles of 32 tokens
+    for E in (1, 63, 256, 1024):                           # a workspace for T tokens serves every smaller call
+        sizes = [f(t, E) for t in [*range(5000), 16383, 65535, 65536, 1 << 20, 16773120]]
+        assert sizes == sorted(sizes)
+    assert [f(1100, e) for e in range(1, 1025)] == sorted(f(1100, e) for e in range(1, 1025))
 
 
 RB = dict(logits=FAKE, kind=0, ids=FAKE, d_weights=FAKE, d_logits=FAKE, T=100, E=64, k=8, score=0, renorm=1, scale=1.0)
