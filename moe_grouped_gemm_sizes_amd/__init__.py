@@ -5,13 +5,16 @@ the HIP kernels behind the C ABI declared in include/moegg.h:
   - scheduler: counts -> padding accounting + tile list;
   - contiguous, masked and K-grouped GEMMs;
   - the layer around them: routing, token permutation, 8-bit activation checkpoints.
-PyTorch supplies device memory and the current stream.  If the library has
-not been built, `lib()` raises.  There is no CPU fallback.
+PyTorch supplies device memory and the current stream.  The layer calls check
+their tensors in a native pass (csrc/args.cpp).  If the library has not been
+built, `lib()` raises.  There is no CPU fallback.
 """
 from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import os
 from dataclasses import dataclass
 from typing import List, Optional, Sequence, Tuple
@@ -598,22 +601,27 @@ def route_workspace(T: int, E: int, device="cuda") -> torch.Tensor:
 _ABSENT = (None, "", None, None)                             # an optional tensor that was not given
 
 
+def _args_module():
+    """The tensor checks of csrc/args.cpp.  Raises if they have not been built."""
+    global _args
+    if _args is None:
+        path = os.path.join(_HERE, "_args.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with python -m moe_grouped_gemm_sizes_amd.build")
+        loader = importlib.machinery.ExtensionFileLoader("_args", path)
+        _args = importlib.util.module_from_spec(importlib.util.spec_from_loader("_args", loader))
+        loader.exec_module(_args)
+    return _args
+
+
+_args = None
+
+
 def _pointers(*specs):
-    """Data pointers of (tensor, name, shape, dtype) specs; None for _ABSENT.  One pass where each is a contiguous
-    tensor as specified on one GPU; else the checks one by one, for their messages."""
-    out = []
-    try:
-        dev = specs[0][0].get_device()
-        for t, _, shape, dtype in specs:
-            if shape is None:
-                out.append(None)
-            elif t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-                out.append(t.data_ptr())
-            else:
-                break
-    except AttributeError:                                   # not a tensor
-        dev = -1
-    if dev >= 0 and len(out) == len(specs):
+    """Data pointers of (tensor, name, shape, dtype) specs; None for _ABSENT.  One native pass where each is a
+    contiguous tensor as specified on one GPU; else the checks one by one, for their messages."""
+    out = (_args or _args_module()).pointers(specs)
+    if out is not None:
         return out
     for t, name, shape, dtype in specs:
         if shape is not None:
@@ -624,9 +632,11 @@ def _pointers(*specs):
 
 def _matrix(t, name: str, dtypes):
     """Shape of a matrix of one of `dtypes`."""
-    if not (isinstance(t, torch.Tensor) and t.dim() == 2 and t.dtype in dtypes):
-        _need(t, name, (None, None), dtypes)
-    return t.shape
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes:
+        shape = t.shape
+        if len(shape) == 2:
+            return shape
+    _need(t, name, (None, None), dtypes)
 
 
 _F, _H, _I = torch.float32, torch.bfloat16, torch.int32

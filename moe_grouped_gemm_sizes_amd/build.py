@@ -1,4 +1,4 @@
-"""Build libmoegg.so in-tree with hipcc for gfx950 only.
+"""Build libmoegg.so in-tree with hipcc for gfx950 only, and the binding's _args module with g++.
 
 Usage: python -m moe_grouped_gemm_sizes_amd.build
 """
@@ -9,12 +9,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoegg.so")
 SOURCES = ["api.hip", "layer_api.hip", "sched.hip", "gemm.hip", "route.hip", "permute.hip", "checkpoint.hip"]
+ARGS = os.path.join(HERE, "_args.so")
 ARCH = "gfx950"
 
 # Packed fp32 VALU ops are switched off for all device code.
@@ -42,10 +44,30 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_args() -> None:
+    """The Python binding's tensor checks (csrc/args.cpp), against torch's headers."""
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    tmp = ARGS + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", "-Wno-unused-function",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           os.path.join(CSRC, "args.cpp"), "-o", tmp, "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for args.cpp:\n{r.stderr}")
+    os.replace(tmp, ARGS)
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(OBJ, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        args = ex.submit(_build_args)
         objs = list(ex.map(_compile, SOURCES))
+        args.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)

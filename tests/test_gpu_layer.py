@@ -751,3 +751,18 @@ def test_another_stream():
     a, b = snapshot(s), snapshot(want)
     for n in a:
         assert torch.equal(a[n], b[n]), n
+
+
+def test_native_tensor_checks():
+    f = mg._args_module().pointers
+    x = torch.zeros(3, 4, device="cuda")
+    y = torch.zeros(5, dtype=torch.int32, device="cuda")
+    e = torch.zeros(0, 4, device="cuda")
+    good = (x, "x", (3, 4), torch.float32)
+    assert f((good, mg._ABSENT, (y, "y", (5,), torch.int32))) == (x.data_ptr(), None, y.data_ptr())
+    assert f(((x, "x", x.shape, x.dtype),)) == (x.data_ptr(),)       # torch.Size is a tuple
+    assert f(((e, "e", (0, 4), torch.float32),)) == (e.data_ptr(),)
+    for bad in [(x, "x", (3, 5), torch.float32), (x, "x", (3,), torch.float32), (x, "x", (3, 4, 1), torch.float32),
+                (x, "x", (3, 4), torch.int32), (x, "x", (3, 2 ** 64 + 4), torch.float32), (x, "x", (3, 4.0), torch.float32),
+                (x.t(), "x", (4, 3), torch.float32), (x[:, :2], "x", (3, 2), torch.float32), (x.cpu(), "x", (3, 4), torch.float32)]:
+        assert f((bad,)) is None and f((good, bad)) is None and f((bad, good)) is None

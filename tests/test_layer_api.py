@@ -244,3 +244,15 @@ def test_small_route_workspace():
     a = tensors("route")
     with pytest.raises(ValueError, match="ws: 0 bytes"):
         mg.route(**{**a, "ws": a["ws"][:0]})
+
+
+def test_native_tensor_checks_want_gpu_tensors():
+    """The one-pass check answers None for whatever does not hold; the named checks follow it."""
+    f = mg._args_module().pointers
+    x = t(3, 4)
+    assert f(()) == () and f((mg._ABSENT, mg._ABSENT)) == (None, None)
+    for spec in [(x, "x", (3, 4), F32), (None, "x", (3, 4), F32), ([1.0], "x", (1,), F32), (x, "x", [3, 4], F32),
+                 (x, "x", (3, 4), "float32"), (x, "x", (3, 4)), (x.to("meta"), "x", (3, 4), F32),
+                 (x.to_sparse(), "x", (3, 4), F32)]:
+        assert f((spec,)) is None and f((mg._ABSENT, spec)) is None
+    assert f([mg._ABSENT]) is None
