@@ -12,7 +12,7 @@
 // of earlier tokens with the same expert.  No order of atomics enters: inside
 // a 64-token step each expert has a 64-bit mask of its tokens (set by OR), and
 // a rank is a popcount of the bits below; steps add up in LDS, token tiles
-// through a [tiles, E] table of 16-bit counts.  Up to 16 tokens, one workgroup
+// through a [tiles, E] table of 16-bit counts.  For a few tokens, one workgroup
 // does everything in one launch; beyond, route_kernel leaves ranks inside the
 // tile in row_of, and route_rows_kernel, whose every workgroup sums the table,
 // adds the segment start and the earlier tiles.
@@ -34,10 +34,6 @@
 namespace moegg {
 
 constexpr int kStep = 64;                 // tokens that share one round of masks
-// Tokens of a call that one workgroup does by itself.  16 tokens over 64 experts
-// take 4.6 us so and 7.2 us in two launches, over 256 experts in groups 9.5 us both;
-// 32 tokens 6.3 against 7.1 and 14 against 9.7 us.
-constexpr int kOneLaunch = 16;
 constexpr float kFltMax = 3.402823466e+38f;
 
 // What routing reads as a logit: NaN is no expert, +inf the largest number.
@@ -666,6 +662,17 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackwardArgs a
 
 // ----------------------------------------------------------------- launches
 
+// Tokens that one workgroup does by itself, a wave for each at first.  In one and in
+// two launches (us, k = 8): 64 experts 24 tokens 5.3 and 6.6, 32 tokens 6.3 and 6.6,
+// 48 tokens 8.0 and 6.6; 256 experts 32 tokens 8.3 and 7.4, but a second launch costs
+// the host 2.2; with a bias 64 experts 24 tokens 6.3 and 7.1, 32 tokens 7.8 and 7.1,
+// 256 experts 20 tokens 9.0 and 8.7; in groups 16 tokens 9.0 and 9.6, 17 tokens 9.3.
+template <int VPL, int MODE>
+static int one_launch_tokens(const RouteArgs& a) {
+    if (a.n_groups > 1 || VPL > 4) return 16;
+    return MODE == 0 ? 32 : (VPL <= 2 ? 24 : 16);
+}
+
 template <int VPL, int MODE>
 static hipError_t route_as(const RouteArgs& a, hipStream_t s) {
     Groups gr{1, 0, 0};
@@ -679,7 +686,7 @@ static hipError_t route_as(const RouteArgs& a, hipStream_t s) {
     // groups off whole lanes: a wave has E doubles of LDS, at most 32 KB for all of them
     const int most = std::min(route_threads(VPL) / 64, gr.in_lanes || a.E <= 256 ? 16 : (a.E <= 512 ? 8 : 4));
     const size_t lds = gr.in_lanes ? 0 : sizeof(double) * (size_t)a.E;
-    if (a.T <= kOneLaunch) {
+    if (a.T <= one_launch_tokens<VPL, MODE>(a)) {        // at most kStep
         const int waves = a.T < 4 ? 4 : (a.T < most ? a.T : most);
         route_kernel<VPL, MODE, true><<<1, waves * 64, lds * waves, s>>>(a, gr);
         return hipGetLastError();

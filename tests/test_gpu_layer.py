@@ -198,7 +198,7 @@ def test_route_long_call_is_deterministic_and_counts_up():
     assert np.array_equal(a["row_of"].cpu().numpy().reshape(-1), row)
 
 
-@pytest.mark.parametrize("T,E,n", [(16, 96, 1), (17, 96, 3), (255, 256, 8), (1024, 40, 1), (1025, 129, 1), (2500, 512, 8),
+@pytest.mark.parametrize("T,E,n", [(16, 96, 1), (17, 96, 3), (24, 128, 1), (25, 64, 1), (32, 250, 1), (33, 60, 1), (255, 256, 8), (1024, 40, 1), (1025, 129, 1), (2500, 512, 8),
                                    (3500, 260, 2), (4097, 64, 4)])
 def test_route_sizes_around_the_tiles(T, E, n):
     l = torch.randn(T, E, generator=gen(T)).to(BF16).cuda()
