@@ -593,7 +593,9 @@ size_t moegg_route_workspace_bytes(int T, int E);
  *   n_groups, topk_groups, group_top: experts in n_groups groups of E /
  *            n_groups consecutive ids; only the topk_groups groups with the
  *            largest sums of their group_top (1 or 2) largest scores (keys, with
- *            a bias) take part, ties to the lower group.  n_groups = 1: all.
+ *            a bias) take part, ties to the lower group.  Experts that cannot be
+ *            chosen have no score: a group with one other has that one's, and a
+ *            group with none comes after all that have any.  n_groups = 1: all.
  *   weights  fp32 [T, k], written: scale * s[id], divided by the token's sum of
  *            chosen scores when renorm is not 0; 0 where ids is -1.
  *   m_sizes  int32 [E], written: assignments of every expert.  With cap they

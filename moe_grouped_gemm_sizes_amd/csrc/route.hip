@@ -286,7 +286,8 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, const Groups& gr
             __builtin_amdgcn_wave_barrier();
         }
         merge_lanes(gr.lg, t1, t2);
-        const double score = a.group_top == 2 ? t1 + t2 : t1;
+        // of the scores that there are: a group with one has that one, a group with none -inf, which no other has
+        const double score = a.group_top == 2 && t2 > -__builtin_inf() ? t1 + t2 : t1;
         // A group's lanes compare it with L groups at a time: its rank is the number of better ones.
         int rank = 0;
         for (int o0 = 0; o0 < a.n_groups; o0 += L) {

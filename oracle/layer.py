@@ -52,7 +52,9 @@ def route(logits, k: int, score: str = "softmax", bias=None, n_groups: int = 1, 
         if n_groups > 1:
             # a group of single best experts is ordered by their keys, a sum of two by scores (with the bias)
             gk = key if b is not None or group_top == 1 else [s[t, e] if ok[e] else -np.inf for e in range(E)]
-            g = [sum(sorted(gk[i * gs:(i + 1) * gs], reverse=True)[:group_top]) for i in range(n_groups)]
+            # of the scores that there are; a group without any is below all others
+            have = [[x for x in gk[i * gs:(i + 1) * gs] if x > -np.inf] for i in range(n_groups)]
+            g = [sum(sorted(x, reverse=True)[:group_top]) if x else -np.inf for x in have]
             kept = sorted(range(n_groups), key=lambda i: (-g[i], i))[:topk_groups]
         cand = [e for e in range(E) if e // gs in kept and ok[e]]
         pick = sorted(cand, key=lambda e: (-key[e], e))[:k]
