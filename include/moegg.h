@@ -645,7 +645,9 @@ moegg_status_t moegg_route_backward(const void* logits, moegg_logits_t logits_dt
  *            with an infinity s is infinite (E8M0: 255) and the codes 0 or NaN.
  * Rows that no token has keep their contents.  A token is read once, whatever k.
  * bf16: any K >= 1, pointers 2-byte aligned.  e4m3: K % 128 == 0, x and A
- * 16-byte aligned, A_scale 4-byte aligned.  k = 1..32.
+ * 16-byte aligned, A_scale 4-byte aligned.  k = 1..32.  This and the two calls
+ * below: T * k < 2^31, widths up to 2^30 and T * ceil(width / 512) up to
+ * 33553407; UNSUPPORTED beyond.
  */
 moegg_status_t moegg_dispatch(const void* x, const int32_t* row_of, void* A, void* A_scale, int T, int k, int K,
                               int64_t rows_total, moegg_dtype_t dtype, void* stream);

@@ -60,7 +60,8 @@ moegg_status_t check_permute(const int32_t* row_of, int T, int k, int W, int64_t
     if (T < 0 || k < 1 || W < 1 || rows < 0 || rows > INT32_MAX) return MOEGG_ERR_INVALID_ARG;
     if (T > 0 && !row_of) return MOEGG_ERR_INVALID_ARG;
     if (!aligned(row_of, 4)) return MOEGG_ERR_INVALID_ARG;
-    if (k > kRouteMaxTopK) return MOEGG_ERR_UNSUPPORTED;
+    // columns are 32-bit, and go up to 8191 past the width
+    if (k > kRouteMaxTopK || W > 1 << 30) return MOEGG_ERR_UNSUPPORTED;
     if ((int64_t)T * k > INT32_MAX) return MOEGG_ERR_UNSUPPORTED;
     // a wave for each token and 512 columns, and up to 256 workgroups of 4 more
     if (((int64_t)T * (((int64_t)W + 511) / 512) + 1024) * 64 > kMaxWorkItems) return MOEGG_ERR_UNSUPPORTED;
