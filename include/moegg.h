@@ -638,8 +638,9 @@ moegg_status_t moegg_route_backward(const void* logits, moegg_logits_t logits_dt
  *            of MOEGG_FP8_E4M3_FP4_E2M1): e4m3 codes, with A_scale as that call
  *            takes it: per 1x128 group
  *                s = amax / 448 (1 if that is 0), codes e4m3_rne(x / s), with
- *            s and the quotient rounded to fp32 (the other calls that quantize
- *            take a quotient within 2 ulp);
+ *            s and the quotient rounded to fp32 (so has the checkpoint of
+ *            moegg_swiglu_checkpoint; the other codes that the calls below make
+ *            have a quotient within 2 ulp);
  *            E8M0: s rounded up to a power of two, at least 2^-126.
  *            A NaN is the code NaN and does not count for the amax; in a group
  *            with an infinity s is infinite (E8M0: 255) and the codes 0 or NaN.
@@ -688,7 +689,7 @@ moegg_status_t moegg_combine_backward(const void* dout, const void* Y, const flo
  *            scales [rows_total, I/128] (MOEGG_FP8_E4M3) or [I/128, rows_total]
  *            (MOEGG_FP8_E4M3_SCALE_KM).
  *   ckpt     e4m3 [rows_total, 2I], ckpt_scale fp32 [rows_total, 2I/128]: GU's
- *            codes and 1x128 scales, as moegg_dispatch quantizes.
+ *            codes and 1x128 scales, the same as moegg_dispatch's.
  *   m_sizes  int32 [G]: the first sum_e max(m_e, 0) rows (at most rows_total) are
  *            read and written; the others keep their contents.  Segments lie
  *            back to back (seg_align 1), as in the K-grouped calls.

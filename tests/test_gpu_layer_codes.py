@@ -1,0 +1,69 @@
+"""e4m3 codes and fp32 scales of bf16 values, and of bf16 values times a weight, on MI355X: equal to what
+s = amax / 448 (1 where that is 0) and e4m3_rne(x / s) give with both divisions rounded to fp32 (+0 and -0 are equal).
+
+bf16 values over a bf16 maximum lie on e4m3's rounding borders, or within an ulp of them, once in two hundred, so that a
+quotient 2 ulp off takes another code there.  The CPU's divisions are correctly rounded."""
+import pytest
+import torch
+
+import moe_grouped_gemm_sizes_amd as mg
+from tests.test_gpu_layer import BF16, E4M3, gen, operand
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    mg.lib()
+
+
+def values(rows, width, seed):
+    """bf16 values with groups of zeros, of subnormal and tiny scales, and of large ones."""
+    x = torch.randn(rows, width, generator=gen(seed))
+    x[0, :128] = 0
+    x[1, :128] *= 1e-36
+    x[2, :128] = 1e-40
+    x[3, :128] *= 1e36
+    x[4, :128] *= 2.0 ** -101
+    return x.to(BF16)
+
+
+def codes(v, s):
+    return (v / s).clamp(-448, 448).to(E4M3).float()
+
+
+def scale(amax):
+    s = amax / 448
+    return torch.where(s > 0, s, torch.ones_like(s))
+
+
+def row_operand(v):
+    """fp32 [R, W] -> the codes' values and scales of 1x128 groups."""
+    g = v.reshape(v.shape[0], -1, 128)
+    s = scale(g.abs().amax(-1))
+    return codes(g, s[..., None]).reshape(v.shape), s
+
+
+def borders(v, s):
+    """Values whose quotient is within 2^-22 of a border between two codes (above e4m3's subnormals)."""
+    q = v.double() / s.double()
+    m = torch.frexp(q)[0].abs() * 16 % 1                    # a border has 4 bits after the leading one, the last set
+    return int((((m - 0.5).abs() < 2.0 ** -18) & (q.abs() > 2.0 ** -6)).sum())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "rows", "km"])
+def test_checkpoint_codes_are_those_of_dispatch(fmt):
+    R, I = 300, 640
+    gu = values(R, 2 * I, 31)
+    want, s = row_operand(gu.float())
+    assert borders(gu.float().reshape(R, -1, 128), s[..., None]) > 500
+    H, hs = operand((R,), R, I, fmt)
+    ck, cs = operand((R,), R, 2 * I, "rows")
+    mg.swiglu_checkpoint(gu.cuda(), torch.tensor([R], dtype=torch.int32).cuda(), H, ck, cs, hs, scale_km=fmt == "km")
+    assert torch.equal(cs.cpu(), s)
+    assert torch.equal(ck.cpu().float(), want)
+    A, A_scale = operand((R,), R, 2 * I, "rows")
+    mg.dispatch(gu.cuda(), torch.arange(R, dtype=torch.int32).view(R, 1).cuda(), A, A_scale)
+    assert torch.equal(A_scale, cs) and torch.equal(A.view(torch.uint8), ck.view(torch.uint8))
