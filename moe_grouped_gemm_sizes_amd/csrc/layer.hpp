@@ -283,9 +283,10 @@ __device__ __forceinline__ GroupScale group_scale(float amax) {
 // x / s.  The product with the hardware's reciprocal (1 ulp) is within 2 ulp;
 // EXACT adds the rest of the reciprocal before it rounds, which leaves 2^-45: in
 // effect the rounded quotient.  bf16 values against a bf16 maximum meet e4m3's
-// rounding borders exactly (one value in two hundred of normal data), and there the
-// last bit decides the code: dispatch and the SwiGLU checkpoint take EXACT.  Values
-// that are computed in fp32 do so once in 2^20, and take the product.
+// rounding borders exactly (one value in two hundred of normal data), both times a
+// weight within an ulp, and there the last bit decides the code: dispatch, combine's
+// backward pass and the SwiGLU checkpoint take EXACT.  Values that have no such
+// common factor do so once in 2^20, and take the product.
 template <bool EXACT>
 __device__ __forceinline__ float quotient(float x, float inv, float low) {
     return EXACT ? __builtin_fmaf(x, inv, x * low) : x * inv;

@@ -67,3 +67,28 @@ def test_checkpoint_codes_are_those_of_dispatch(fmt):
     A, A_scale = operand((R,), R, 2 * I, "rows")
     mg.dispatch(gu.cuda(), torch.arange(R, dtype=torch.int32).view(R, 1).cuda(), A, A_scale)
     assert torch.equal(A_scale, cs) and torch.equal(A.view(torch.uint8), ck.view(torch.uint8))
+
+
+@pytest.mark.parametrize("fmt", ["rows", "km", "e8m0"])
+def test_combine_backward_codes(fmt):
+    """dY = w * dout, rounded to fp32: a common factor leaves the quotients near where they were."""
+    T, k, N = 60, 3, 1152
+    dout = values(T, N, 32)
+    w = torch.rand(T, k, generator=gen(33))
+    w[7] = torch.tensor([1.0, 0.0, 0.5])
+    w[8] = torch.tensor([-0.7, 2.0 ** -20, 3.0])
+    v = (w[:, :, None] * dout.float()[:, None, :]).reshape(T * k, N)
+    Y = torch.randn(T * k, N, generator=gen(34)).to(BF16)
+    dY, sc = operand((T * k,), T * k, N, fmt)
+    dw = torch.empty(T, k, device="cuda")
+    mg.combine_backward(dout.cuda(), Y.cuda(), w.cuda(), torch.arange(T * k, dtype=torch.int32).view(T, k).cuda(), dY, dw,
+                        sc, scale_km=fmt == "km")
+    want, s = row_operand(v)
+    if fmt == "e8m0":                                       # the power of two that is at least s
+        m, e = torch.frexp(s)
+        e = torch.where(m == 0.5, e - 1, e).clamp(min=-126)
+        assert torch.equal(sc.t().cpu().int(), e + 127)
+        want = codes(v.reshape(T * k, -1, 128), torch.ldexp(torch.ones_like(s), e)[..., None]).reshape(v.shape)
+    else:
+        assert torch.equal((sc.t() if fmt == "km" else sc).cpu(), s)
+    assert torch.equal(dY.cpu().float(), want)
