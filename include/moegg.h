@@ -638,9 +638,10 @@ moegg_status_t moegg_route_backward(const void* logits, moegg_logits_t logits_dt
  *            of MOEGG_FP8_E4M3_FP4_E2M1): e4m3 codes, with A_scale as that call
  *            takes it: per 1x128 group
  *                s = amax / 448 (1 if that is 0), codes e4m3_rne(x / s), with
- *            s and the quotient rounded to fp32 (so have moegg_combine_backward
- *            and the checkpoint of moegg_swiglu_checkpoint; the other codes that
- *            the calls below make have a quotient within 2 ulp);
+ *            s and the quotient rounded to fp32 (so have moegg_combine_backward,
+ *            the checkpoint of moegg_swiglu_checkpoint and bf16 rows of
+ *            moegg_checkpoint_to_k_groups; the other codes that the calls below
+ *            make have a quotient within 2 ulp);
  *            E8M0: s rounded up to a power of two, at least 2^-126.
  *            A NaN is the code NaN and does not count for the amax; in a group
  *            with an infinity s is infinite (E8M0: 255) and the codes 0 or NaN.

@@ -253,14 +253,15 @@ __device__ __forceinline__ void reduce_rows(const float (&v)[N], float (&out)[N 
     }
 }
 
-// A column's scale: pre and inverse into LDS, the scale itself to k_scale.
+// A column's scale: pre, inverse and (not NULL) what that is short into LDS, the scale itself to k_scale.
 // tiny: some column has a pre that is not 1.
 template <bool E8M0>
-__device__ __forceinline__ void column_scale(float amax, float* pre, float* inv, int* tiny, void* k_scale, int64_t at,
-                                             bool store) {
+__device__ __forceinline__ void column_scale(float amax, float* pre, float* inv, float* low, int* tiny, void* k_scale,
+                                             int64_t at, bool store) {
     const GroupScale g = group_scale<E8M0>(amax);
     *pre = g.pre;
     *inv = g.inv;
+    if (low) *low = g.low;
     if (g.pre != 1.f) *tiny = 1;
     if (store) {
         if (E8M0) ((uint8_t*)k_scale)[at] = (uint8_t)g.byte;
@@ -268,19 +269,23 @@ __device__ __forceinline__ void column_scale(float amax, float* pre, float* inv,
     }
 }
 
-template <int N>
-__device__ __forceinline__ void quantize_columns(const float* v, const float* pre, const float* inv, bool tiny,
-                                                 uint32_t (&q)[N / 4]) {
+// low: what the inverses are short of (EXACT: the rounded quotient), else not of use.
+template <int N, bool EXACT>
+__device__ __forceinline__ void quantize_columns(const float* v, const float* pre, const float* inv, const float* low,
+                                                 bool tiny, uint32_t (&q)[N / 4]) {
     if (!tiny) {
 #pragma unroll
         for (int i = 0; i < N; i += 4)
-            q[i / 4] = e4m3_x4(v[i] * inv[i], v[i + 1] * inv[i + 1], v[i + 2] * inv[i + 2], v[i + 3] * inv[i + 3]);
+            q[i / 4] = e4m3_x4(quotient<EXACT>(v[i], inv[i], low[i]), quotient<EXACT>(v[i + 1], inv[i + 1], low[i + 1]),
+                               quotient<EXACT>(v[i + 2], inv[i + 2], low[i + 2]),
+                               quotient<EXACT>(v[i + 3], inv[i + 3], low[i + 3]));
     } else {
 #pragma unroll
         for (int i = 0; i < N; i += 4)
-            q[i / 4] = e4m3_x4(tiny_quotient(v[i], pre[i], inv[i]), tiny_quotient(v[i + 1], pre[i + 1], inv[i + 1]),
-                               tiny_quotient(v[i + 2], pre[i + 2], inv[i + 2]),
-                               tiny_quotient(v[i + 3], pre[i + 3], inv[i + 3]));
+            q[i / 4] = e4m3_x4(tiny_quotient<EXACT>(v[i], pre[i], inv[i], low[i]),
+                               tiny_quotient<EXACT>(v[i + 1], pre[i + 1], inv[i + 1], low[i + 1]),
+                               tiny_quotient<EXACT>(v[i + 2], pre[i + 2], inv[i + 2], low[i + 2]),
+                               tiny_quotient<EXACT>(v[i + 3], pre[i + 3], inv[i + 3], low[i + 3]));
     }
 }
 
@@ -395,10 +400,10 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_fp8_kernel(Checkpoin
         if (c < kBwdCols) {
             const int l = c >> 4, i = c & 15;            // lane l: 8 gate columns, then the 8 up columns 16 further on
             const int col = 32 * (l >> 1) + 8 * (l & 1) + (i < 8 ? i : i + 8);
-            column_scale<E8M0>(y, &pre_s[c], &inv_s[c], &tiny_s, a.k_scale,
+            column_scale<E8M0>(y, &pre_s[c], &inv_s[c], nullptr, &tiny_s, a.k_scale,
                                (int64_t)want * (2 * a.W) + unit * kBwdCols + col, store);
         } else {
-            column_scale<E8M0>(y, &pre_s[c], &inv_s[c], &tiny_s, a.hk_scale,
+            column_scale<E8M0>(y, &pre_s[c], &inv_s[c], nullptr, &tiny_s, a.hk_scale,
                                (int64_t)want * a.W + unit * 64 + c - kBwdCols, store);
         }
     }
@@ -410,8 +415,8 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_fp8_kernel(Checkpoin
     for (int p = 0; p < kBwdPasses; ++p) {
         uint32_t q[4], qh[2];
         asm volatile("" ::: "memory");                   // 24 inverses from LDS again, not in registers beside v
-        quantize_columns<16>(v[p], pre_s + l8 * 16, inv_s + l8 * 16, tiny, q);
-        quantize_columns<8>(v[p] + 16, pre_s + kBwdCols + l8 * 8, inv_s + kBwdCols + l8 * 8, tiny, qh);
+        quantize_columns<16, false>(v[p], pre_s + l8 * 16, inv_s + l8 * 16, inv_s, tiny, q);
+        quantize_columns<8, false>(v[p] + 16, pre_s + kBwdCols + l8 * 8, inv_s + kBwdCols + l8 * 8, inv_s, tiny, qh);
         const uint32_t step = (uint32_t)(p * kBwdRows * upr);
         __builtin_amdgcn_raw_buffer_store_b128(join_codes(u32x2{q[0], q[1]}, u32x2{q[2], q[3]}, odd), k_out,
                                                (int)(at * kBwdCols + l8 * 16), (int)(step * kBwdCols), CP_NT);
@@ -434,7 +439,8 @@ constexpr int kKgRows = kThreads / 16, kKgPasses = 128 / kKgRows, kKgRun = 11;
 template <OperandFormat FMT, bool E8M0>
 __global__ __launch_bounds__(kThreads) void k_groups_kernel(CheckpointArgs a) {
     __shared__ float red_s[kThreads / 64][kUnit];
-    __shared__ float pre_s[kUnit], inv_s[kUnit];
+    constexpr bool EXACT = FMT == kBf16 && !E8M0;        // bf16 values: the rounded quotient (by a power of two it is)
+    __shared__ float pre_s[kUnit], inv_s[kUnit], low_s[EXACT ? kUnit : 1];
     __shared__ int tiny_s;
     constexpr int RAW = FMT == kBf16 ? 2 : 1;
     const int upr = a.W / kUnit;                         // units of a row
@@ -507,8 +513,8 @@ __global__ __launch_bounds__(kThreads) void k_groups_kernel(CheckpointArgs a) {
         float x = 0.f;
 #pragma unroll
         for (int w = 0; w < kThreads / 64; ++w) x = fmaxf(x, red_s[w][c]);
-        column_scale<E8M0>(x, &pre_s[c], &inv_s[c], &tiny_s, a.k_scale, (int64_t)want * a.W + unit * kUnit + c,
-                           want < a.scale_groups);
+        column_scale<E8M0>(x, &pre_s[c], &inv_s[c], EXACT ? &low_s[c] : nullptr, &tiny_s, a.k_scale,
+                           (int64_t)want * a.W + unit * kUnit + c, want < a.scale_groups);
     }
     __syncthreads();
     const bool tiny = tiny_s;
@@ -520,7 +526,7 @@ __global__ __launch_bounds__(kThreads) void k_groups_kernel(CheckpointArgs a) {
 #pragma unroll
         for (int i = 0; i < RAW; ++i) asm volatile("" : "+v"(raw[p][i]));   // scaled anew, not kept in fp32
         values(p, v);
-        quantize_columns<16>(v, pre_s + l16 * 16, inv_s + l16 * 16, tiny, q);
+        quantize_columns<16, EXACT>(v, pre_s + l16 * 16, inv_s + l16 * 16, EXACT ? low_s + l16 * 16 : inv_s, tiny, q);
         __builtin_amdgcn_raw_buffer_store_b128(u32x4{q[0], q[1], q[2], q[3]}, k_out, (int)(at * kUnit + l16 * 16),
                                                (int)(p * kKgRows * upr * kUnit), CP_NT);
     }

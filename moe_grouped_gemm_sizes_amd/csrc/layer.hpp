@@ -285,8 +285,8 @@ __device__ __forceinline__ GroupScale group_scale(float amax) {
 // effect the rounded quotient.  bf16 values against a bf16 maximum meet e4m3's
 // rounding borders exactly (one value in two hundred of normal data), both times a
 // weight within an ulp, and there the last bit decides the code: dispatch, combine's
-// backward pass and the SwiGLU checkpoint take EXACT.  Values that have no such
-// common factor do so once in 2^20, and take the product.
+// backward pass, the SwiGLU checkpoint and bf16 rows into token groups take EXACT.
+// Values that have no such common factor do so once in 2^20, and take the product.
 template <bool EXACT>
 __device__ __forceinline__ float quotient(float x, float inv, float low) {
     return EXACT ? __builtin_fmaf(x, inv, x * low) : x * inv;

@@ -92,3 +92,28 @@ def test_combine_backward_codes(fmt):
     else:
         assert torch.equal((sc.t() if fmt == "km" else sc).cpu(), s)
     assert torch.equal(dY.cpu().float(), want)
+
+
+def test_token_group_codes_of_bf16_rows():
+    counts, M = [300, 0, 128, 5, 77], 512
+    R = sum(counts)
+    x = torch.randn(R, M, generator=gen(35))
+    x[:, 7] = 0
+    x[:, 300] *= 1e-36
+    x[:, 301] *= 1e-38
+    x[:, 302] *= 1e36
+    x = x.to(BF16)
+    S = mg.k_scale_groups(counts)
+    X_k, ks = torch.empty(R, M, dtype=torch.uint8, device="cuda").view(E4M3), torch.empty(S, M, device="cuda")
+    mg.checkpoint_to_k_groups(x.cuda(), torch.tensor(counts, dtype=torch.int32).cuda(), X_k, ks)
+    at = n = near = 0
+    for c in counts:
+        for r in range(at, at + c, 128):
+            v = x[r:min(r + 128, at + c)].float()
+            s = scale(v.abs().amax(0))
+            near += borders(v, s)
+            assert torch.equal(ks[n].cpu(), s)
+            assert torch.equal(X_k.cpu()[r:r + v.shape[0]].float(), codes(v, s))
+            n += 1
+        at += c
+    assert n == S and near > 500
