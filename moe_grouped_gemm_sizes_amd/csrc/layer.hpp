@@ -169,16 +169,6 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
     v = max(v, dpp<DPP_BCAST31>(0, v));
     return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
-__device__ __forceinline__ float wave_max(float v) {
-    constexpr float lo = -__builtin_inff();
-    v = fmaxf(v, dpp_f<DPP_SHR + 1>(lo, v));
-    v = fmaxf(v, dpp_f<DPP_SHR + 2>(lo, v));
-    v = fmaxf(v, dpp_f<DPP_SHR + 4>(lo, v));
-    v = fmaxf(v, dpp_f<DPP_SHR + 8>(lo, v));
-    v = fmaxf(v, dpp_f<DPP_BCAST15>(lo, v));
-    v = fmaxf(v, dpp_f<DPP_BCAST31>(lo, v));
-    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
-}
 // row_bcast hands a row's sum to the next rows only: with bound lanes reading
 // 0, lane 63 sums rows 0..3 in a fixed order.
 __device__ __forceinline__ float wave_sum(float v) {
