@@ -213,8 +213,9 @@ __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v 
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
 // 1 / (1 + e^-x) by the hardware's exp2 and reciprocal (1 ulp each).  The
-// rounded product x log2 e costs |x| 2^-24 relative at most, 1e-6 at |x| = 16;
-// its users round the result to 8 or 4 bits.  Below 2^-126 the reciprocal is 0.
+// rounded product x log2 e costs |x| 2^-24 relative at most, and the constant,
+// 0.22 2^-24 off, a quarter of that: 1.2e-6 at |x| = 16; its users round the
+// result to 8 or 4 bits.  Below 2^-126 the reciprocal is 0.
 __device__ __forceinline__ float sigmoid_fast(float x) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * -1.44269504f));
 }
