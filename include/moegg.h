@@ -606,7 +606,8 @@ size_t moegg_route_workspace_bytes(int T, int E);
  *            tokens with expert e; -1 where ids is -1, where r >= cap, and for
  *            rows at or past rows_total.
  * Keys with a bias, and sums of two scores, are compared in 64 bits.
- * Deterministic.  One launch up to 16 tokens, or up to 32 without bias and groups; else two.
+ * Deterministic.  One launch up to 16 tokens; without groups, up to 32 over at
+ * most 256 experts without a bias and up to 24 over at most 128 with one; else two.
  * T = 0..16773120, E = 1..1024, k = 1..32 (and k <= E): UNSUPPORTED beyond
  * the upper ends.  n_groups divides E, at most 64; 1 <= topk_groups <=
  * n_groups; group_top 1 or 2; scale > 0 and finite; seg_align >= 1; cap >= 0;
