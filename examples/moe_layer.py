@@ -8,7 +8,7 @@ MoELayer.forward / backward is a training step in fp8 (e4m3 operands with fp32 s
 
 What forward keeps for backward: the fp8 input rows (hidden + hidden / 32 bytes a row) and the fp8 gate/up columns
 (2 inter + inter / 16), a little over half of what bf16 would take, plus the router's choice.  MoELayer.decode is
-the same layer without a checkpoint for a few tokens: five launches that a graph can capture.
+the same layer without a checkpoint for a few tokens: five calls that a graph can capture.
 """
 from __future__ import annotations
 
@@ -86,7 +86,7 @@ class MoELayer:
         return out, dict(r, x=x, A=A, A_scale=A_scale, ckpt=ckpt, ckpt_scale=ckpt_scale, Y=Y)
 
     def backward(self, dout, kept):
-        """Gradients of x (bf16), the router (fp32) and the expert weights: W1 fp32 [E, hidden, 2 inter] and W2
+        """Gradients of x (bf16), the router (a bf16 product, as fp32) and the expert weights: W1 fp32 [E, hidden, 2 inter] and W2
         [E, inter, hidden], as the K-grouped product writes them."""
         T, rows, I, K, E = dout.shape[0], dout.shape[0] * self.k, self.inter, self.hidden, self.E
         m, row_of = kept["m_sizes"], kept["row_of"]

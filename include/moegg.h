@@ -565,6 +565,13 @@ moegg_status_t moegg_grouped_gemm_k_grouped_e8m0(
  * through [G, cap]: row e * cap + r is row r of expert e, and rows_total is
  * G * cap.  A row_of value outside [0, rows_total) is read as "none".  Each row
  * belongs to at most one (t, j).
+ *
+ * Two things end at the checkpoint calls.  Their segments lie back to back, as in
+ * the K-grouped calls: rows that moegg_route lays out with seg_align > 1 or cap
+ * serve the other GEMMs only, and nothing here can tell or refuse them.  And their
+ * row scales are fp32: moegg_dispatch and moegg_combine_backward write E8M0
+ * operands for the products, but no checkpoint call reads or makes E8M0 rows
+ * (their token-group scales may be E8M0).
  */
 
 /* Scores of the router's logits. */
@@ -642,7 +649,7 @@ moegg_status_t moegg_route_backward(const void* logits, moegg_logits_t logits_dt
  *            s and the quotient rounded to fp32 (so have moegg_combine_backward,
  *            the checkpoint of moegg_swiglu_checkpoint and bf16 rows of
  *            moegg_checkpoint_to_k_groups; the other codes that the calls below
- *            make have a quotient within 2 ulp);
+ *            make have a quotient within 2 ulp); a zero may lose its sign;
  *            E8M0: s rounded up to a power of two, at least 2^-126.
  *            A NaN is the code NaN and does not count for the amax; in a group
  *            with an infinity s is infinite (E8M0: 255) and the codes 0 or NaN.
@@ -695,7 +702,9 @@ moegg_status_t moegg_combine_backward(const void* dout, const void* Y, const flo
  *   m_sizes  int32 [G]: the first sum_e max(m_e, 0) rows (at most rows_total) are
  *            read and written; the others keep their contents.  Segments lie
  *            back to back (seg_align 1), as in the K-grouped calls.
- * I % 128 == 0; GU, H and ckpt 16-byte aligned, scales 4.
+ * I % 128 == 0; GU, H and ckpt 16-byte aligned, scales 4.  UNSUPPORTED:
+ * MOEGG_FP8_E4M3_E8M0, I > 2^21, and (rows_total / 128 + G) * (I / 128) past
+ * 1047551 (the fp8 backward call: 4193279).
  */
 moegg_status_t moegg_swiglu_checkpoint(const void* GU, const int32_t* m_sizes, void* H, void* H_scale, void* ckpt,
                                        float* ckpt_scale, int G, int64_t rows_total, int I, moegg_dtype_t dtype,
@@ -742,7 +751,8 @@ moegg_status_t moegg_swiglu_checkpoint_backward_fp8(
  * column and token group, X_k_scale [scale_groups, M], fp32 or (k_e8m0) E8M0
  * bytes.  So the fp8 input of the forward product is what a training step
  * keeps of it.  Values are code * scale in fp32.  Rows and token groups as
- * above.  M % 256 == 0; X and X_k 16-byte aligned, scales 4.
+ * above.  M % 256 == 0; X and X_k 16-byte aligned, scales 4.  UNSUPPORTED:
+ * MOEGG_FP8_E4M3_E8M0, M > 2^21, (rows_total / 128 + G) * (M / 256) past 8387583.
  */
 moegg_status_t moegg_checkpoint_to_k_groups(const void* X, const float* X_scale, const int32_t* m_sizes, void* X_k,
                                             void* X_k_scale, int G, int64_t rows_total, int M, int64_t scale_groups,
