@@ -86,8 +86,8 @@ class MoELayer:
         return out, dict(r, x=x, A=A, A_scale=A_scale, ckpt=ckpt, ckpt_scale=ckpt_scale, Y=Y)
 
     def backward(self, dout, kept):
-        """Gradients of x (bf16), the router (a bf16 product, as fp32) and the expert weights: W1 fp32 [E, hidden, 2 inter] and W2
-        [E, inter, hidden], as the K-grouped product writes them."""
+        """Gradients of x (bf16), the router (a bf16 product, as fp32) and the expert weights: W1 fp32 [E, hidden,
+        2 inter] and W2 [E, inter, hidden], as the K-grouped product writes them."""
         T, rows, I, K, E = dout.shape[0], dout.shape[0] * self.k, self.inter, self.hidden, self.E
         m, row_of = kept["m_sizes"], kept["row_of"]
         dY, dY_scale = self._fp8(rows, K)

@@ -171,9 +171,9 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(PermuteArgs a, int ch
 // A workgroup takes a token: dY rows are weight * dout, and each weight's
 // gradient is the dot product of its row of Y with dout, summed in fp32 in a
 // fixed order (lane pieces, wave, waves).  dout is read once per 8 rows.  32768
-// rows of 7168 in bf16: 182 us, 5.5 TB/s, and with e4m3 dY 143 us (row-major
-// scales) and 151 us (transposed ones); as many waves as there are 512-column
-// pieces, since 4 waves going round take 202 us.
+// rows of 7168 in bf16: 181 us, 5.5 TB/s; with e4m3 dY 143 us (row-major scales),
+// 151 us (transposed) and 146 us (E8M0), 167 to 174 us where dout comes from HBM.
+// As many waves as there are 512-column pieces: 4 waves going round take 202 us.
 template <OperandFormat FMT>
 __global__ __launch_bounds__(1024) void combine_backward_kernel(PermuteArgs a) {
     // Rows loaded at a time.  With quantization beside them, 8 leave one workgroup a CU at 7168 columns (158 us), 2
