@@ -432,11 +432,11 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_fp8_kernel(Checkpoin
 // times.  The codes (or bf16 values) stay in registers as they were read, and
 // are scaled twice: for the columns' maxima and for the new codes.  32768 rows of
 // 7168 columns: 85 us, 5.7 TB/s, in runs of 11 units to an XCD (of 8: 89 us, of 16:
-// 90 us; odd runs from 3 to 13 within 2 us); 92 us with the rounded quotient, which
-// bf16 rows take for 0.5 us.  In runs of 8, cached accesses took
+// 90 us; odd runs from 3 to 13 within 2 us).  In runs of 8, cached accesses took
 // 94 us and values kept in fp32 between the two 100 us.  bf16 loads are not
 // streamed: each takes the halves of lines, which would then be fetched twice (4096
-// columns: 75 us, 82 us streamed).
+// columns: 74 us, 82 us streamed).  bf16 rows take the rounded quotient, at no cost
+// that shows; e4m3 rows would take 92 us with it.
 constexpr int kKgRows = kThreads / 16, kKgPasses = 128 / kKgRows, kKgRun = 11;
 
 template <OperandFormat FMT, bool E8M0>
@@ -521,6 +521,15 @@ __global__ __launch_bounds__(kThreads) void k_groups_kernel(CheckpointArgs a) {
     }
     __syncthreads();
     const bool tiny = tiny_s;
+    // EXACT's 32 numbers of a lane's columns stay in registers (512 columns: 11.2 us, read in each pass 13.2 us)
+    float inv[16], low[16];
+    if (EXACT) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            inv[i] = inv_s[l16 * 16 + i];
+            low[i] = low_s[l16 * 16 + i];
+        }
+    }
     auto k_out = make_rsrc(a.k_out + u * kUnit, units * kUnit);
 #pragma unroll
     for (int p = 0; p < kKgPasses; ++p) {
@@ -529,7 +538,8 @@ __global__ __launch_bounds__(kThreads) void k_groups_kernel(CheckpointArgs a) {
 #pragma unroll
         for (int i = 0; i < RAW; ++i) asm volatile("" : "+v"(raw[p][i]));   // scaled anew, not kept in fp32
         values(p, v);
-        quantize_columns<16, EXACT>(v, pre_s + l16 * 16, inv_s + l16 * 16, EXACT ? low_s + l16 * 16 : inv_s, tiny, q);
+        if (EXACT) quantize_columns<16, true>(v, pre_s + l16 * 16, inv, low, tiny, q);
+        else quantize_columns<16, false>(v, pre_s + l16 * 16, inv_s + l16 * 16, inv_s, tiny, q);
         __builtin_amdgcn_raw_buffer_store_b128(u32x4{q[0], q[1], q[2], q[3]}, k_out, (int)(at * kUnit + l16 * 16),
                                                (int)(p * kKgRows * upr * kUnit), CP_NT);
     }
