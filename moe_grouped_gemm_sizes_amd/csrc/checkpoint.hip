@@ -11,6 +11,7 @@
 
 #include "device.hpp"
 #include "layer.hpp"
+#include "rows.hpp"
 
 namespace moegg {
 
@@ -29,25 +30,6 @@ __device__ __forceinline__ void split_codes(u32x4 c, bool odd, u32x2& g, u32x2& 
     const u32x2 got = {lane_of<DPP_XOR1>(send.x), lane_of<DPP_XOR1>(send.y)};
     g = odd ? got : lo;
     u = odd ? hi : got;
-}
-
-__device__ __forceinline__ void unpack8(u32x4 v, float* f) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = bf16_lo(v[i]);
-        f[2 * i + 1] = bf16_hi(v[i]);
-    }
-}
-__device__ __forceinline__ u32x4 pack8(const float* f) {
-    u32x4 v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-    return v;
-}
-__device__ __forceinline__ float amax8(const float* f, float m) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
-    return m;
 }
 
 // One scale of a row-major operand: group kg of row `row`.
