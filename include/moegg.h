@@ -758,6 +758,140 @@ moegg_status_t moegg_checkpoint_to_k_groups(const void* X, const float* X_scale,
                                             void* X_k_scale, int G, int64_t rows_total, int M, int64_t scale_groups,
                                             moegg_dtype_t dtype, int k_e8m0, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The block around the layer: the norm in front of it, the router's training
+ * loss, and low-rank adapters beside its projections.  The conventions at the
+ * top hold for these calls too; none sets flags.  Every output is the same
+ * bits each time.
+ */
+
+/* Storage type of a norm's weight. */
+typedef enum { MOEGG_WEIGHT_FP32 = 0, MOEGG_WEIGHT_BF16 = 1 } moegg_weight_t;
+
+/*
+ * Root-mean-square norm with the residual's addition, its result in bf16 and
+ * in the operand format of a grouped GEMM (of a shared expert, for one).
+ *   x, residual  bf16 [T, K]; residual NULL: 0.
+ *   sum_out      bf16 [T, K] or NULL: h = bf16_rne(x + residual), which the norm
+ *                goes by.  Without a residual h is x, and sum_out is NULL.  It may
+ *                be x or residual itself.
+ *   rstd         fp32 [T] or NULL: 1 / sqrt(mean of h^2 + eps), which the backward
+ *                pass reads.
+ *   y            bf16 [T, K] or NULL: bf16_rne(h * rstd * weight).
+ *   q, q_scale   q_dtype MOEGG_FP8_E4M3, MOEGG_FP8_E4M3_SCALE_KM or
+ *                MOEGG_FP8_E4M3_E8M0: e4m3 codes [T, K] of h * rstd * weight (fp32)
+ *                and their scales as for moegg_dispatch's A, with a quotient within 2
+ *                ulp.  MOEGG_BF16: NULL, and y is not.
+ *   weight       fp32 or bf16 [K].
+ * The squares are summed in fp32; a row past its range is summed scaled, so that
+ * every finite row has its norm.  A row with an infinity has rstd 0, NaN where the
+ * infinity is and 0 elsewhere; a row with a NaN is NaN.
+ * K = 1..32768 (UNSUPPORTED beyond), K % 128 == 0 with q; T up to 2097151; eps
+ * from 2^-126 up, finite.  With q x, residual, sum_out, y, q and weight are 16-byte
+ * aligned, else bf16 2, fp32 4; scales 4.
+ */
+moegg_status_t moegg_rms_norm(const void* x, const void* residual, const void* weight, moegg_weight_t weight_dtype,
+                              float eps, void* sum_out, void* y, void* q, void* q_scale, float* rstd, int T, int K,
+                              moegg_dtype_t q_dtype, void* stream);
+
+/* Workspace bytes of moegg_rms_norm_backward for up to T tokens of K columns.  Pure
+ * host function.  Returns 0 for invalid arguments. */
+size_t moegg_rms_norm_workspace_bytes(int T, int K);
+
+/*
+ * Backward pass of moegg_rms_norm.  dy bf16 [T, K] is the gradient of y (or of what
+ * q stands for), h its sum_out (or x), rstd as it was written; d_sum bf16 [T, K] or
+ * NULL the gradient that arrives at the sum itself.  With xhat = h * rstd and
+ * g = dy * weight, in fp32:
+ *     dx = bf16_rne(d_sum + rstd * (g - xhat * mean(g * xhat))),
+ * the gradient of x and of the residual alike, and
+ *     d_weight[c] = sum over rows of dy * xhat
+ * in fp32, in a fixed order.  d_weight NULL: not computed, and ws may be NULL.
+ *   dx may be dy, h or d_sum itself.
+ * Two launches with d_weight, else one.  K and T as above; bf16 2-byte and fp32
+ * 4-byte aligned; ws: moegg_rms_norm_workspace_bytes(T, K), 256-byte aligned.
+ */
+moegg_status_t moegg_rms_norm_backward(const void* dy, const void* h, const void* weight, moegg_weight_t weight_dtype,
+                                       const float* rstd, const void* d_sum, void* dx, float* d_weight, int T, int K,
+                                       void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of moegg_balance_loss for up to T tokens, E experts and S
+ * sequences.  Pure host function.  Returns 0 for invalid arguments. */
+size_t moegg_balance_loss_workspace_bytes(int T, int E, int S);
+
+/*
+ * The router's balance loss of every sequence, its z loss, and the counts of its
+ * experts.
+ *   logits       as for moegg_route [T, E]; NaN and -inf: p is 0; +inf is read as the
+ *                largest finite number.
+ *   ids          int32 [T, k] as moegg_route writes them; outside [0, E): none.
+ *   seq_offsets  int32 [S + 1]: sequence s is tokens seq_offsets[s] up to
+ *                seq_offsets[s + 1]; the offsets do not fall, and are read as within
+ *                [0, T].  Tokens before the first or after the last belong to no
+ *                sequence.  Padding between sequences is a sequence of its own whose
+ *                loss is left out.  NULL (S = 1): all tokens are one.  Offsets that
+ *                fall make results of no meaning; nothing is read or written out of
+ *                bounds.
+ * With n the sequence's tokens and p a token's softmax (MOEGG_SCORE_SOFTMAX) or its
+ * sigmoids over their sum (MOEGG_SCORE_SIGMOID), 0 for a token without experts:
+ *   counts       int32 [S, E]: assignments c_e of every expert.
+ *   probs        fp32 [S, E] or NULL: P_e = mean of p_e over the tokens.
+ *   loss         fp32 [S]: E / (k n) * sum_e c_e P_e (1 for a perfect balance).
+ *   z_loss       fp32 [S] or NULL: mean of (ln sum_e e^logit)^2, 0 for a token
+ *                without experts; inf past fp32's range.  Softmax only (UNSUPPORTED
+ *                otherwise).
+ * A sequence of no tokens has 0 everywhere.  p in fp32; sums over tokens in fp32
+ * inside a tile of them, then in 64 bits, in a fixed order.  Two launches.
+ * T = 0..16773120, E = 1..1024, k = 1..32 (and k <= E), S = 1..65536: UNSUPPORTED
+ * beyond the upper ends; tensors aligned to their elements.
+ * ws: moegg_balance_loss_workspace_bytes(T, E, S), 256-byte aligned.
+ */
+moegg_status_t moegg_balance_loss(const void* logits, moegg_logits_t logits_dtype, const int32_t* ids,
+                                  const int32_t* seq_offsets, float* loss, float* z_loss, int32_t* counts, float* probs,
+                                  int T, int E, int k, int S, moegg_score_t score, void* ws, size_t ws_bytes,
+                                  void* stream);
+
+/*
+ * Gradient of the logits from those of loss and z_loss (the counts have none):
+ *   d_logits     [T, E] of the logits' type, every element written: the gradient,
+ *                plus `before` ([T, E] of the same type, or NULL; it may be d_logits
+ *                itself), so that what moegg_route_backward wrote is kept.
+ *   counts       as moegg_balance_loss wrote them, with the same k, S, seq_offsets
+ *                and score; d_loss fp32 [S]; d_z_loss fp32 [S] or NULL (softmax only).
+ * Tokens of no sequence get `before`, or 0.
+ */
+moegg_status_t moegg_balance_loss_backward(const void* logits, moegg_logits_t logits_dtype, const int32_t* counts,
+                                           const int32_t* seq_offsets, const float* d_loss, const float* d_z_loss,
+                                           const void* before, void* d_logits, int T, int E, int k, int S,
+                                           moegg_score_t score, void* stream);
+
+/* Workspace bytes of moegg_lora for up to T rows of K columns and a rank of R.  Pure
+ * host function.  Returns 0 for invalid arguments. */
+size_t moegg_lora_workspace_bytes(int T, int K, int R);
+
+/*
+ * Low-rank adapters of many requests at once, beside a projection that they share
+ * (moegg_grouped_gemm_contiguous with one expert, or any other):
+ *     out[t] = bf16_rne(Y[t] + scale[a] * (X[t] A_a^T) B_a^T),  a = adapter[t].
+ *   X        bf16 [T, K], the projection's input; Y bf16 [T, N], its output.
+ *   A        bf16 [L, R, K]; B bf16 [L, N, R]: adapters of a smaller rank are filled
+ *            up with zeros.
+ *   scale    fp32 [L], or NULL: all 1.
+ *   adapter  int32 [T], rows in any order; outside [0, L): no adapter, out[t] = Y[t].
+ *   out      bf16 [T, N]; it may be Y itself, whose rows without an adapter are then
+ *            not touched.
+ * The inner product is summed in fp32 and enters the outer one as two bf16 (to
+ * 2^-16 of it); scale and Y come in fp32, with one rounding at the end.  Only
+ * adapters that some row has are read.  Two launches.
+ * K, N and R are multiples of 8, R = 8..128, T up to 2^24 and T / 64 * N / 256 up to
+ * 2^23: UNSUPPORTED otherwise.  X, A, B, Y and out 16-byte aligned, scale and adapter 4.
+ * ws: moegg_lora_workspace_bytes(T, K, R), 256-byte aligned.
+ */
+moegg_status_t moegg_lora(const void* X, const void* A, const void* B, const float* scale, const int32_t* adapter,
+                          const void* Y, void* out, int T, int K, int N, int R, int L, void* ws, size_t ws_bytes,
+                          void* stream);
+
 /* Copy the stats of the last scheduled call on `ws` to the host.
  * Synchronizes `stream`. */
 moegg_status_t moegg_stats_read(const void* ws, moegg_stats_t* h_out, void* stream);

@@ -4,7 +4,8 @@ The binding only marshals arguments.  Every step of the grouped GEMM runs in
 the HIP kernels behind the C ABI declared in include/moegg.h:
   - scheduler: counts -> padding accounting + tile list;
   - contiguous, masked and K-grouped GEMMs;
-  - the layer around them: routing, token permutation, 8-bit activation checkpoints.
+  - the layer around them: routing, token permutation, 8-bit activation checkpoints;
+  - the block around that: RMS norm, the router's balance loss, low-rank adapters.
 PyTorch supplies device memory and the current stream.  The layer calls check
 their tensors in a native pass (csrc/args.cpp).  If the library has not been
 built, `lib()` raises.  There is no CPU fallback.
@@ -34,6 +35,7 @@ FLAG_SCALE_GROUPS = 0x10
 FLAG_SYNC_TIMEOUT = 0x20
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 LOGITS_FP32, LOGITS_BF16 = 0, 1
+WEIGHT_FP32, WEIGHT_BF16 = 0, 1
 Q_VALUES = (8, 16, 32, 64, 128, 256)
 BLOCK_M_PER_EXPERT = -1          # per-expert tile heights (include/moegg.h)
 
@@ -143,6 +145,14 @@ EXPORTS = {
     "moegg_swiglu_checkpoint_backward_fp8": (_I32, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _I64,
                                                     _I32, _I64, _I32, _I32, _VP]),
     "moegg_checkpoint_to_k_groups": (_I32, [_VP, _VP, _VP, _VP, _VP, _I32, _I64, _I32, _I64, _I32, _I32, _VP]),
+    "moegg_rms_norm": (_I32, [_VP, _VP, _VP, _I32, _F32, _VP, _VP, _VP, _VP, _VP, _I32, _I32, _I32, _VP]),
+    "moegg_rms_norm_workspace_bytes": (_SZ, [_I32, _I32]),
+    "moegg_rms_norm_backward": (_I32, [_VP, _VP, _VP, _I32, _VP, _VP, _VP, _VP, _I32, _I32, _VP, _SZ, _VP]),
+    "moegg_balance_loss_workspace_bytes": (_SZ, [_I32, _I32, _I32]),
+    "moegg_balance_loss": (_I32, [_VP, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _I32, _I32, _I32, _I32, _VP, _SZ, _VP]),
+    "moegg_balance_loss_backward": (_I32, [_VP, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _I32, _I32, _I32, _I32, _VP]),
+    "moegg_lora_workspace_bytes": (_SZ, [_I32, _I32, _I32]),
+    "moegg_lora": (_I32, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _I32, _I32, _I32, _I32, _VP, _SZ, _VP]),
     "moegg_stats_read": (_I32, [_VP, ctypes.POINTER(_Stats), _VP]),
     "moegg_stats_report": (_I32, [ctypes.POINTER(_Stats), ctypes.POINTER(_Report)]),
     "moegg_tile_list_read": (_I32, [_VP, ctypes.POINTER(_Tile), _I64, ctypes.POINTER(_I64), _VP]),
@@ -826,6 +836,163 @@ def checkpoint_to_k_groups(X, m_sizes, X_k, X_k_scale, X_scale=None, *, scale_km
                                     (X_k_scale, "X_k_scale", (S, M), kind))
     _check(lib().moegg_checkpoint_to_k_groups(px, ps, pm, pk, pks, G, rows, M, S, code, kind is torch.uint8,
                                               _stream(stream)), "moegg_checkpoint_to_k_groups")
+
+
+# ---------------------------------------------------------------- the block around the layer
+
+
+def _workspace_of(n: int, device) -> torch.Tensor:
+    if n == 0:
+        raise ValueError("invalid workspace request")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _ws_spec(ws, need: int, what: str):
+    """ws' size in bytes, and its spec."""
+    n = ws.numel() if isinstance(ws, torch.Tensor) else 0
+    if n < need:
+        raise ValueError(f"ws: {n} bytes, need {need} ({what})")
+    return n, (ws, "ws", (n,), torch.uint8)
+
+
+def _optional(t, name: str, shape, kind):
+    return (t, name, shape, kind) if t is not None else _ABSENT
+
+
+def _norm_weight(weight, K: int):
+    """Type code of a norm's weight, and its spec."""
+    kind = weight.dtype if isinstance(weight, torch.Tensor) else None
+    if kind is not _H and kind is not _F:
+        _need(weight, "weight", (K,), (_F, _H))
+    return WEIGHT_BF16 if kind is _H else WEIGHT_FP32, (weight, "weight", (K,), kind)
+
+
+def rms_norm(x, weight, *, y=None, q=None, q_scale=None, residual=None, sum_out=None, rstd=None, eps: float = 1e-6,
+             scale_km: bool = False, stream=None):
+    """h = x + residual (bf16, to sum_out), then h * rstd * weight with rstd = 1 / sqrt(mean h^2 + eps) (see moegg.h):
+    as y bf16 [T, K], and as q e4m3 [T, K] with the scales of the grouped GEMM that reads it: fp32 [T, K/128],
+    [K/128, T] (scale_km), or uint8 E8M0 bytes [K/128, T].  x, residual, sum_out bf16 [T, K]; weight fp32 or bf16 [K];
+    rstd fp32 [T].  y or q, or both; sum_out may be x or residual."""
+    T, K = _matrix(x, "x", (_H,))
+    weight_kind, weight_spec = _norm_weight(weight, K)
+    if q is None:
+        _none(q_scale, "q_scale", "without q")
+        if y is None:
+            raise ValueError("y or q expected")
+        if scale_km:
+            raise ValueError("scale_km applies to e4m3 operands with fp32 scales")
+        code, q_spec, scale_spec = BF16, _ABSENT, _ABSENT
+    else:
+        _matrix(q, "q", (_E4M3,))
+        _, code, q_spec, scale_spec = _row_operand(q, "q", q_scale, K, scale_km)
+        q_spec = (q, "q", (T, K), _E4M3)
+        if q.shape[0] != T:
+            _need(q, "q", (T, K), (_E4M3,))
+    if residual is None:
+        _none(sum_out, "sum_out", "without a residual")
+    px, pr, pw, ps, py, pq, pqs, pd = _pointers(
+        (x, "x", (T, K), _H), _optional(residual, "residual", (T, K), _H), weight_spec,
+        _optional(sum_out, "sum_out", (T, K), _H), _optional(y, "y", (T, K), _H), q_spec, scale_spec,
+        _optional(rstd, "rstd", (T,), _F))
+    _check(lib().moegg_rms_norm(px, pr, pw, weight_kind, eps, ps, py, pq, pqs, pd, T, K, code, _stream(stream)),
+           "moegg_rms_norm")
+
+
+@functools.lru_cache(maxsize=4096)
+def rms_norm_workspace_bytes(T: int, K: int) -> int:
+    return int(lib().moegg_rms_norm_workspace_bytes(T, K))
+
+
+def rms_norm_workspace(T: int, K: int, device="cuda") -> torch.Tensor:
+    return _workspace_of(rms_norm_workspace_bytes(T, K), device)
+
+
+def rms_norm_backward(dy, h, weight, rstd, dx, d_weight=None, ws=None, *, d_sum=None, stream=None):
+    """dx bf16 [T, K], the gradient of x and of the residual, and d_weight fp32 [K] (None: left out) from dy bf16 [T, K]
+    (see moegg.h); h is rms_norm's sum_out (or x), rstd as it wrote it, d_sum bf16 [T, K] the gradient that arrives at the
+    sum itself.  ws: rms_norm_workspace(T, K), or of more tokens; needed for d_weight.  dx may be dy, h or d_sum."""
+    T, K = _matrix(dy, "dy", (_H,))
+    weight_kind, weight_spec = _norm_weight(weight, K)
+    n, ws_spec = 0, _ABSENT
+    if d_weight is not None:
+        n, ws_spec = _ws_spec(ws, rms_norm_workspace_bytes(T, K), f"rms_norm_workspace_bytes({T}, {K})")
+    pd, ph, pw, pr, ps, px, pdw, pws = _pointers(
+        (dy, "dy", (T, K), _H), (h, "h", (T, K), _H), weight_spec, (rstd, "rstd", (T,), _F),
+        _optional(d_sum, "d_sum", (T, K), _H), (dx, "dx", (T, K), _H), _optional(d_weight, "d_weight", (K,), _F), ws_spec)
+    _check(lib().moegg_rms_norm_backward(pd, ph, pw, weight_kind, pr, ps, px, pdw, T, K, pws, n, _stream(stream)),
+           "moegg_rms_norm_backward")
+
+
+@functools.lru_cache(maxsize=4096)
+def balance_loss_workspace_bytes(T: int, E: int, S: int = 1) -> int:
+    return int(lib().moegg_balance_loss_workspace_bytes(T, E, S))
+
+
+def balance_loss_workspace(T: int, E: int, S: int = 1, device="cuda") -> torch.Tensor:
+    return _workspace_of(balance_loss_workspace_bytes(T, E, S), device)
+
+
+def balance_loss(logits, ids, loss, counts, ws, *, probs=None, z_loss=None, seq_offsets=None,
+                 score: int = SCORE_SOFTMAX, stream=None):
+    """The router's balance loss [S] of every sequence from logits [T, E] and the ids [T, k] that route chose, with its
+    counts int32 [S, E], mean probabilities probs fp32 [S, E] and z_loss fp32 [S] (see moegg.h).  seq_offsets int32
+    [S + 1]: the sequences' bounds; None: all tokens are one.  ws: balance_loss_workspace(T, E, S), or of more."""
+    T, E = _matrix(logits, "logits", (_F, _H))
+    k = _matrix(ids, "ids", (_I,))[1]
+    S = _matrix(counts, "counts", (_I,))[0]
+    kind = logits.dtype
+    n, ws_spec = _ws_spec(ws, balance_loss_workspace_bytes(T, E, S), f"balance_loss_workspace_bytes({T}, {E}, {S})")
+    if seq_offsets is None and S != 1:
+        raise ValueError(f"seq_offsets: int32 [{S + 1}] expected for counts of {S} sequences")
+    l, i, o, pl, pz, pc, pp, pw = _pointers(
+        (logits, "logits", (T, E), kind), (ids, "ids", (T, k), _I), _optional(seq_offsets, "seq_offsets", (S + 1,), _I),
+        (loss, "loss", (S,), _F), _optional(z_loss, "z_loss", (S,), _F), (counts, "counts", (S, E), _I),
+        _optional(probs, "probs", (S, E), _F), ws_spec)
+    _check(lib().moegg_balance_loss(l, LOGITS_BF16 if kind is _H else LOGITS_FP32, i, o, pl, pz, pc, pp, T, E, k, S,
+                                    score, pw, n, _stream(stream)), "moegg_balance_loss")
+
+
+def balance_loss_backward(logits, counts, d_loss, d_logits, *, k: int, d_z_loss=None, seq_offsets=None,
+                          score: int = SCORE_SOFTMAX, before=None, stream=None):
+    """d_logits [T, E] (logits' type) from d_loss [S] and d_z_loss [S], added to `before` [T, E], which may be d_logits
+    (see moegg.h); counts as balance_loss wrote them, k the experts of a token."""
+    T, E = _matrix(logits, "logits", (_F, _H))
+    S = _matrix(counts, "counts", (_I,))[0]
+    kind = logits.dtype
+    if seq_offsets is None and S != 1:
+        raise ValueError(f"seq_offsets: int32 [{S + 1}] expected for counts of {S} sequences")
+    l, c, o, dl, dz, b, d = _pointers(
+        (logits, "logits", (T, E), kind), (counts, "counts", (S, E), _I),
+        _optional(seq_offsets, "seq_offsets", (S + 1,), _I), (d_loss, "d_loss", (S,), _F),
+        _optional(d_z_loss, "d_z_loss", (S,), _F), _optional(before, "before", (T, E), kind),
+        (d_logits, "d_logits", (T, E), kind))
+    _check(lib().moegg_balance_loss_backward(l, LOGITS_BF16 if kind is _H else LOGITS_FP32, c, o, dl, dz, b, d, T, E, k, S,
+                                             score, _stream(stream)), "moegg_balance_loss_backward")
+
+
+@functools.lru_cache(maxsize=4096)
+def lora_workspace_bytes(T: int, K: int, R: int) -> int:
+    return int(lib().moegg_lora_workspace_bytes(T, K, R))
+
+
+def lora_workspace(T: int, K: int, R: int, device="cuda") -> torch.Tensor:
+    return _workspace_of(lora_workspace_bytes(T, K, R), device)
+
+
+def lora(X, A, B, adapter, Y, out, ws, *, scale=None, stream=None):
+    """out[t] = Y[t] + scale[a] * (X[t] A_a^T) B_a^T with a = adapter[t], or Y[t] where that is no adapter (see moegg.h).
+    X bf16 [T, K], Y and out bf16 [T, N] (out may be Y), A bf16 [L, R, K], B bf16 [L, N, R], adapter int32 [T], scale
+    fp32 [L].  ws: lora_workspace(T, K, R), or of more rows."""
+    T, K = _matrix(X, "X", (_H,))
+    N = _matrix(Y, "Y", (_H,))[1]
+    if not isinstance(A, torch.Tensor) or A.dim() != 3:
+        _need(A, "A", (None, None, K), (_H,))
+    L, R = A.shape[0], A.shape[1]
+    n, ws_spec = _ws_spec(ws, lora_workspace_bytes(T, K, R), f"lora_workspace_bytes({T}, {K}, {R})")
+    px, pa, pb, ps, pi, py, po, pw = _pointers(
+        (X, "X", (T, K), _H), (A, "A", (L, R, K), _H), (B, "B", (L, N, R), _H), _optional(scale, "scale", (L,), _F),
+        (adapter, "adapter", (T,), _I), (Y, "Y", (T, N), _H), (out, "out", (T, N), _H), ws_spec)
+    _check(lib().moegg_lora(px, pa, pb, ps, pi, py, po, T, K, N, R, L, pw, n, _stream(stream)), "moegg_lora")
 
 
 def stats_read(ws: torch.Tensor, stream=None) -> Stats:

@@ -15,7 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoegg.so")
-SOURCES = ["api.hip", "layer_api.hip", "sched.hip", "gemm.hip", "route.hip", "permute.hip", "checkpoint.hip"]
+SOURCES = ["api.hip", "layer_api.hip", "block_api.hip", "sched.hip", "gemm.hip", "route.hip", "permute.hip",
+           "checkpoint.hip", "norm.hip", "balance.hip", "lora.hip"]
 ARGS = os.path.join(HERE, "_args.so")
 ARCH = "gfx950"
 

@@ -1,0 +1,101 @@
+// block.hpp -- arguments and launchers of the operators of a block around the
+// MoE layer: RMS norm (norm.hip), the router's balance loss (balance.hip) and
+// low-rank adapters (lora.hip), which the C ABI (block_api.hip) calls.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "layer.hpp"
+
+namespace moegg {
+
+constexpr int kNormMaxWidth = 32768;     // columns of a row that one workgroup holds in registers
+constexpr int kNormMaxParts = 256;       // partial sums of the weight's gradient
+constexpr int kBalanceMaxExperts = 1024;
+constexpr int kBalanceMaxSequences = 65536;
+constexpr int kLoraChunk = 64;           // rows whose adapters one wave looks at together
+constexpr int kLoraMaxRank = 128;
+constexpr int kLoraMaxRows = 1 << 24;
+
+struct NormArgs {
+    const void* x;                       // forward: bf16 [T, K]; backward: h
+    const void* residual;                // forward: bf16 [T, K] or NULL; backward: d_sum
+    const void* weight;                  // fp32 or bf16 [K]
+    const void* dy;                      // backward: bf16 [T, K]
+    void* sum_out;                       // bf16 [T, K] or NULL
+    void* y;                             // forward: bf16 [T, K] or NULL; backward: dx
+    void* q;                             // e4m3 [T, K] or NULL
+    void* q_scale;
+    float* rstd;                         // [T]; forward: or NULL
+    float* d_weight;                     // backward: [K] or NULL
+    float* parts;                        // backward: [norm_parts(T), K]
+    int T, K;
+    int weight_bf16;
+    float eps;
+    OperandFormat fmt;                   // of q; kBf16: none
+};
+
+struct BalanceArgs {
+    const void* logits;                  // fp32 or bf16 [T, E]
+    const int32_t* ids;                  // [T, k]
+    const int32_t* offsets;              // [S + 1] or NULL: one sequence of all tokens
+    float* loss;                         // [S]
+    float* z_loss;                       // [S] or NULL
+    int32_t* counts;                     // [S, E]
+    float* probs;                        // [S, E] or NULL
+    float* part_p;                       // [pieces, E]: sums of probabilities
+    int32_t* part_n;                     // [pieces, E]: assignments
+    float* part_z;                       // [pieces]
+    int T, E, k, S, bf16, sigmoid;
+    int tile_tokens;                     // tokens of one workgroup
+};
+
+struct BalanceBackwardArgs {
+    const void* logits;
+    const int32_t* counts;
+    const int32_t* offsets;
+    const float* d_loss;                 // [S]
+    const float* d_z;                    // [S] or NULL
+    const void* before;                  // logits' type [T, E] or NULL
+    void* d_logits;
+    int T, E, k, S, bf16, sigmoid;
+};
+
+struct LoraArgs {
+    const void* X;                       // bf16 [T, K]
+    const void* A;                       // bf16 [L, R, K]
+    const void* B;                       // bf16 [L, N, R]
+    const float* scale;                  // [L] or NULL
+    const int32_t* adapter;              // [T]
+    const void* Y;                       // bf16 [T, N]
+    void* out;                           // bf16 [T, N]
+    float* U;                            // [splits, T, R]
+    int T, K, N, R, L;
+    int splits;                          // of K
+};
+
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s);
+hipError_t launch_rms_norm_backward(const NormArgs& a, hipStream_t s);
+hipError_t launch_balance_loss(const BalanceArgs& a, hipStream_t s);
+hipError_t launch_balance_loss_backward(const BalanceBackwardArgs& a, hipStream_t s);
+hipError_t launch_lora(const LoraArgs& a, hipStream_t s);
+
+// Partial sums that the norm's backward pass leaves: one a workgroup, and no more
+// workgroups than CUs.
+inline int norm_parts(int T) { return T < kNormMaxParts ? T : kNormMaxParts; }
+
+// Tokens of one workgroup of the balance loss.
+inline int balance_tile_tokens(int T) {
+    const int t = (T + 255) / 256;
+    return t <= 32 ? 32 : (t + 15) / 16 * 16;
+}
+
+// Parts of K that workgroups of the adapters' first product take: 512 columns or more each, and no more of
+// them than make 512 workgroups.
+inline int lora_splits(int T, int K) {
+    const int chunks = (T + kLoraChunk - 1) / kLoraChunk, most = (K + 511) / 512;
+    const int want = chunks > 0 ? (512 + chunks - 1) / chunks : 1;
+    return most < want ? most : want;
+}
+
+}  // namespace moegg
