@@ -14,6 +14,9 @@ constexpr int kNormMaxParts = 256;       // partial sums of the weight's gradien
 constexpr int kBalanceMaxExperts = 1024;
 constexpr int kBalanceMaxSequences = 65536;
 constexpr int kLoraChunk = 64;           // rows whose adapters one wave looks at together
+constexpr int kLoraChunkRows = 256;      // rows up to which chunks are taken as they come
+constexpr int kLoraWindow = 8192;        // rows that one workgroup sorts by adapter
+constexpr int kLoraMaxSorted = 16384;    // adapters whose counts are 64 KB of LDS
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraMaxRows = 1 << 24;
 
@@ -70,8 +73,12 @@ struct LoraArgs {
     const void* Y;                       // bf16 [T, N]
     void* out;                           // bf16 [T, N]
     float* U;                            // [splits, T, R]
+    int32_t* order;                      // [T]: rows by adapter, window by window
+    int4* tiles;                         // [windows, max_tiles]: adapter, first place in `order`, rows
+    int32_t* n_tiles;                    // [windows]
     int T, K, N, R, L;
     int splits;                          // of K
+    int max_tiles;                       // of a window, or of a chunk
 };
 
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s);
@@ -90,12 +97,24 @@ inline int balance_tile_tokens(int T) {
     return t <= 32 ? 32 : (t + 15) / 16 * 16;
 }
 
-// Parts of K that workgroups of the adapters' first product take: 512 columns or more each, and no more of
-// them than make 512 workgroups.
+// Whether rows are sorted by adapter first, which the counts of all adapters in LDS allow.
+inline bool lora_sorted(int T, int L) { return T > kLoraChunkRows && L < kLoraMaxSorted; }
+
+// Tiles of a window or chunk at most: full ones, and one of fewer rows for each adapter
+// (and for rows without one).
+inline int lora_max_tiles(int T, int L) {
+    const bool sorted = lora_sorted(T, L);
+    const int most = sorted ? kLoraWindow : kLoraChunk, rows = T < most ? T : most;
+    return (sorted ? rows / kLoraChunk : 0) + (L < rows ? L + 1 : rows);
+}
+
+// Parts of K that workgroups of the first product take: 2 units of 128 columns a wave (1 where
+// rows are few), and no more of them than make 512 workgroups of full tiles.
 inline int lora_splits(int T, int K) {
-    const int chunks = (T + kLoraChunk - 1) / kLoraChunk, most = (K + 511) / 512;
-    const int want = chunks > 0 ? (512 + chunks - 1) / chunks : 1;
-    return most < want ? most : want;
+    const int tiles = (T + kLoraChunk - 1) / kLoraChunk, units = (K + 127) / 128;
+    const int want = tiles > 0 ? (512 + tiles - 1) / tiles : 1;
+    const int each = (units + 4 * want - 1) / (4 * want);
+    return (units + 4 * each - 1) / (4 * each);
 }
 
 }  // namespace moegg

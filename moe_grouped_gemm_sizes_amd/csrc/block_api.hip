@@ -39,6 +39,24 @@ moegg_status_t check_balance(const moegg_logits_t& logits_dtype, const moegg_sco
 // Rows of partial sums of any call of up to T tokens and S sequences.
 size_t balance_pieces(int T, int S) { return std::min<size_t>(((size_t)T + 31) / 32, 256) + (size_t)S; }
 
+// Workspace of the adapters' call, which serves every call of fewer rows.
+struct LoraLayout {
+    size_t order, tiles, n_tiles, total;
+};
+LoraLayout lora_layout(int T, int K, int R) {
+    // parts of K times rows: those of 512 full tiles, or T; and no more than a part for 4 units and row
+    const size_t units = ((size_t)K + 127) / 128, rows = T;
+    const size_t parts = std::max(std::min(rows * ((units + 3) / 4), (size_t)1024 * kLoraChunk), rows);
+    const size_t windows = (rows + kLoraWindow - 1) / kLoraWindow;
+    LoraLayout l;
+    l.order = align256(parts * sizeof(float) * (size_t)R);
+    l.tiles = l.order + align256(rows * sizeof(int32_t));
+    // a window's tiles: of one row each, and full ones
+    l.n_tiles = l.tiles + align256((rows + rows / kLoraChunk) * sizeof(int4));
+    l.total = l.n_tiles + align256(std::max<size_t>(windows, 1) * sizeof(int32_t));
+    return l;
+}
+
 }  // namespace
 
 extern "C" {
@@ -163,10 +181,8 @@ moegg_status_t moegg_balance_loss_backward(const void* logits, moegg_logits_t lo
 }
 
 size_t moegg_lora_workspace_bytes(int T, int K, int R) {
-    if (T < 0 || T > kLoraMaxRows || K < 8 || K % 8 != 0 || R < 8 || R % 8 != 0 || R > kLoraMaxRank) return 0;
-    // of any call of up to T rows: parts of K times rows are at most 512 chunks' rows, or T
-    const size_t rows = std::max<size_t>(std::min<size_t>((size_t)T * (((size_t)K + 511) / 512), 512 * kLoraChunk), T);
-    return align256(std::max<size_t>(rows, 1) * sizeof(float) * (size_t)R);
+    if (T < 0 || T > kLoraMaxRows || K < 8 || K > 1 << 30 || K % 8 != 0 || R < 8 || R % 8 != 0 || R > kLoraMaxRank) return 0;
+    return lora_layout(T, K, R).total;
 }
 
 moegg_status_t moegg_lora(const void* X, const void* A, const void* B, const float* scale, const int32_t* adapter,
@@ -177,11 +193,31 @@ moegg_status_t moegg_lora(const void* X, const void* A, const void* B, const flo
     if (!all16({X, A, B, Y, out}) || !all4({scale, adapter})) return MOEGG_ERR_INVALID_ARG;
     if (K % 8 != 0 || N % 8 != 0 || R % 8 != 0 || R > kLoraMaxRank || T > kLoraMaxRows) return MOEGG_ERR_UNSUPPORTED;
     const int64_t chunks = ((int64_t)T + kLoraChunk - 1) / kLoraChunk, panels = ((int64_t)N + 255) / 256;
-    // columns are 32-bit, and go up to 255 past the width; up to 1024 workgroups more than one for each chunk and panel
-    if (K > 1 << 30 || N > 1 << 30 || (chunks * std::max<int64_t>(panels, 1) + 2048) * 256 > kMaxWorkItems)
+    // columns are 32-bit, and go up to 255 past the width; up to 4096 workgroups more than one for each chunk and panel
+    if (K > 1 << 30 || N > 1 << 30 || (chunks * panels + 8192) * 256 > kMaxWorkItems)
         return MOEGG_ERR_UNSUPPORTED;
     if (!ws || !aligned(ws, 256) || ws_bytes < moegg_lora_workspace_bytes(T, K, R)) return MOEGG_ERR_WORKSPACE;
-    LoraArgs a{X, A, B, scale, adapter, Y, out, (float*)ws, T, K, N, R, L, lora_splits(T, K)};
+    const LoraLayout at = lora_layout(T, K, R);
+    unsigned char* w = (unsigned char*)ws;
+    LoraArgs a{};
+    a.X = X;
+    a.A = A;
+    a.B = B;
+    a.scale = scale;
+    a.adapter = adapter;
+    a.Y = Y;
+    a.out = out;
+    a.U = (float*)w;
+    a.order = (int32_t*)(w + at.order);
+    a.tiles = (int4*)(w + at.tiles);
+    a.n_tiles = (int32_t*)(w + at.n_tiles);
+    a.T = T;
+    a.K = K;
+    a.N = N;
+    a.R = R;
+    a.L = L;
+    a.splits = lora_splits(T, K);
+    a.max_tiles = lora_max_tiles(T, L);
     return hip_status(launch_lora(a, (hipStream_t)stream), "low-rank adapters");
 }
 

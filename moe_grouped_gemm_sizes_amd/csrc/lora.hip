@@ -1,11 +1,12 @@
 // lora.hip -- low-rank adapters of many requests, added to a projection's output:
 //     out[t] = Y[t] + scale_a (X[t] A_a^T) B_a^T,   a the adapter of row t.
 //
-// Two products of a rank of 8 to 128, so that rows and weights are moved and little is
-// computed.  The rows of one adapter are found by the kernels themselves: a wave
-// looks at 64 consecutive rows, a lane each, and takes the adapters among them one
-// by one; requests lie in consecutive rows, so that long prompts have one or two
-// there.  Then matrix products in blocks of 16 rows.
+// Two products with a rank of 8 to 128, so that rows and weights are moved and little
+// is computed.  Both take tiles: up to 64 rows with one adapter.  Up to 256 rows the
+// kernels find these by themselves: a wave looks at 64 consecutive rows, a lane
+// each, and takes the adapters among them one by one.  Beyond, a first launch
+// sorts windows of 8192 rows by their adapters, so that an adapter's weights are read
+// for 64 rows together whatever the order of the rows.
 #include <hip/hip_runtime.h>
 
 #include "block.hpp"
@@ -16,52 +17,149 @@
 namespace moegg {
 
 constexpr int kThreads = 256;
-constexpr int kBlocks = kLoraChunk / 16;  // row blocks of a chunk
+constexpr int kTile = kLoraChunk;         // rows of a tile
 
-// The adapters among a chunk's 64 rows, in the order of their first rows.
-struct ChunkRows {
-    int own;                             // this lane's adapter; -1: none, or past the last row
-    uint64_t left;                       // rows whose adapter was not taken yet
-    __device__ __forceinline__ ChunkRows(const LoraArgs& a, int chunk) {
-        const int t = chunk * kLoraChunk + ((int)threadIdx.x & 63);
-        own = t < a.T ? a.adapter[t] : -1;
-        if (own >= a.L) own = -1;
-        left = __ballot(own >= 0);
+// ----------------------------------------------------------------- tiles
+
+// Rows of a window in the order of their adapters, and its tiles.  Rows with one
+// adapter come in any order (an LDS atomic gives them their places): a row's result
+// does not depend on its place.
+__global__ __launch_bounds__(1024) void lora_sort_kernel(LoraArgs a, int copy) {
+    extern __shared__ int count_s[];                         // [L + 1]: rows of each adapter, then their first place
+    __shared__ int rows_s[16], tiles_s[16];
+    constexpr int kEach = kLoraWindow / 1024;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, first = (int)blockIdx.x * kLoraWindow;
+    int4* tiles = a.tiles + (int64_t)blockIdx.x * a.max_tiles;
+    int key[kEach], rank[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int t = first + i * 1024 + (int)threadIdx.x;
+        key[i] = t < a.T ? a.adapter[t] : -2;
+        if (key[i] != -2 || t < a.T) key[i] = (uint32_t)key[i] < (uint32_t)a.L ? key[i] : a.L;
     }
-    // The next adapter and its rows.
-    __device__ __forceinline__ int next(uint64_t& rows) {
-        const int adapter = __builtin_amdgcn_readlane(own, __builtin_ctzll(left));
-        rows = __ballot(own == adapter);
+    for (int k = threadIdx.x; k <= a.L; k += 1024) count_s[k] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        // a wave of one adapter (the rows of a long prompt) adds once
+        const int k0 = __builtin_amdgcn_readfirstlane(key[i]);
+        if (__all(key[i] == k0)) {
+            int base = 0;
+            if (lane == 0 && k0 >= 0) base = atomicAdd(&count_s[k0], 64);
+            rank[i] = __builtin_amdgcn_readfirstlane(base) + lane;
+        } else if (key[i] >= 0) {
+            rank[i] = atomicAdd(&count_s[key[i]], 1);
+        }
+    }
+    __syncthreads();
+    // places and tiles before each adapter: a run of adapters a thread
+    const int per = (a.L + 1024) / 1024, k0 = min((int)threadIdx.x * per, a.L + 1), k1 = min(k0 + per, a.L + 1);
+    int rows = 0, n = 0;
+    for (int k = k0; k < k1; ++k) {
+        rows += count_s[k];
+        if (k < a.L || copy) n += (count_s[k] + kTile - 1) / kTile;
+    }
+    int rows_end = rows, n_end = n;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int r = __shfl_up(rows_end, d, 64), m = __shfl_up(n_end, d, 64);
+        if (lane >= d) {
+            rows_end += r;
+            n_end += m;
+        }
+    }
+    if (lane == 63) {
+        rows_s[wave] = rows_end;
+        tiles_s[wave] = n_end;
+    }
+    __syncthreads();
+    int place = rows_end - rows, tile = n_end - n;
+    for (int w = 0; w < wave; ++w) {
+        place += rows_s[w];
+        tile += tiles_s[w];
+    }
+    for (int k = k0; k < k1; ++k) {
+        const int c = count_s[k];
+        count_s[k] = place;
+        if (k < a.L || copy)
+            for (int b = 0; b < c; b += kTile) tiles[tile++] = int4{k < a.L ? k : -1, first + place + b, min(kTile, c - b), 0};
+        place += c;
+    }
+    if (threadIdx.x == 1023) a.n_tiles[blockIdx.x] = tile;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+        if (key[i] >= 0) a.order[first + count_s[key[i]] + rank[i]] = first + i * 1024 + (int)threadIdx.x;
+}
+
+// The tiles that a workgroup takes: every slots-th one of its chunk or window,
+// their rows listed in LDS.
+template <bool SORTED>
+struct Tiles {
+    int own;                             // chunk: this lane's adapter, -1: none or past the last row
+    uint64_t left;                       // chunk: rows not taken yet
+    int at, end, slots, unit;
+    __device__ __forceinline__ Tiles(const LoraArgs& a, int unit_, int slot, int slots_, bool bare)
+        : at(slot), slots(slots_), unit(unit_) {
+        if (SORTED) {
+            end = a.n_tiles[unit];
+        } else {
+            const int t = unit * kLoraChunk + ((int)threadIdx.x & 63);
+            own = t < a.T ? a.adapter[t] : -2;
+            if (own != -2) own = (uint32_t)own < (uint32_t)a.L ? own : -1;
+            left = __ballot(own >= 0 || (bare && own == -1));
+            for (int i = 0; i < slot && left; ++i) take();
+        }
+    }
+    __device__ __forceinline__ uint64_t take() {
+        const int first = __builtin_amdgcn_readlane(own, __builtin_ctzll(left));
+        const uint64_t rows = __ballot(own == first);
         left &= ~rows;
-        return adapter;
+        return rows;
+    }
+    // The next tile's adapter (-1: rows without one) and number of rows; false: there is none.
+    __device__ __forceinline__ bool next(const LoraArgs& a, int* list_s, int& adapter, int& n) {
+        const int lane = threadIdx.x & 63;
+        if (SORTED) {
+            if (at >= end) return false;
+            const int4 tile = a.tiles[(int64_t)unit * a.max_tiles + at];
+            adapter = __builtin_amdgcn_readfirstlane(tile.x);
+            n = __builtin_amdgcn_readfirstlane(tile.z);
+            if (threadIdx.x < 64) list_s[lane] = a.order[tile.y + min(lane, n - 1)];
+            at += slots;
+        } else {
+            if (!left) return false;
+            adapter = __builtin_amdgcn_readlane(own, __builtin_ctzll(left));
+            const uint64_t rows = take();
+            n = __popcll(rows);
+            if (threadIdx.x < 64 && (rows >> lane & 1))
+                list_s[__popcll(rows & ((1ull << lane) - 1))] = unit * kLoraChunk + lane;
+            for (int i = 1; i < slots && left; ++i) take();
+        }
+        __syncthreads();
+        return true;
     }
 };
 
-// Row (within the chunk) of the i-th set bit of `rows`, for every lane's own i;
-// past the last one the last one's.  Goes through LDS: lane r of the chunk says where it is.
-__device__ __forceinline__ void list_rows(uint64_t rows, int* list_s) {
-    const int lane = threadIdx.x & 63;
-    if (rows >> lane & 1) list_s[__popcll(rows & ((1ull << lane) - 1))] = lane;
-}
-
 // ----------------------------------------------------------------- X A^T
 
-// A workgroup takes the rows of one adapter in a chunk and a part of K, its waves
-// a quarter of that each; their sums meet in LDS.  D = X A^T in blocks of 16 rows x
-// 16 ranks.
+// A workgroup takes a tile and a part of K, its waves a quarter of that each; their
+// sums meet in LDS.  D = X A^T in blocks of 16 rows x 16 ranks.  K goes in units of 128
+// columns, whole lines, all of whose loads are in flight together.
+constexpr int kUnit = 128, kUnitSteps = kUnit / 32;
+
 template <int RT, int CT>
-__device__ __forceinline__ void shrink(const LoraArgs& a, const int* list_s, int n, int adapter, int chunk, int split,
-                                       float (*sum_s)[16][16]) {
+__device__ __forceinline__ void shrink(const LoraArgs& a, const int* list_s, int n, int adapter, int split,
+                                       float (*sum_s)[16][CT * 16 + 4]) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int l16 = lane & 15, grp = lane >> 4;
-    // K in steps of 32, shared out over splits x 4 waves
-    const int steps = (a.K + 31) / 32, shares = a.splits * 4, share = split * 4 + wave;
-    const int s0 = (int)((int64_t)steps * share / shares), s1 = (int)((int64_t)steps * (share + 1) / shares);
+    const int units = (a.K + kUnit - 1) / kUnit, shares = a.splits * 4, share = split * 4 + wave;
+    const int u0 = (int)((int64_t)units * share / shares), u1 = (int)((int64_t)units * (share + 1) / shares);
     const uint16_t* x[RT];
     const uint16_t* w[CT];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
-        x[r] = (const uint16_t*)a.X + ((int64_t)chunk * kLoraChunk + list_s[min(r * 16 + l16, n - 1)]) * a.K + grp * 8;
+        x[r] = (const uint16_t*)a.X + (int64_t)list_s[min(r * 16 + l16, n - 1)] * a.K + grp * 8;
 #pragma unroll
     for (int c = 0; c < CT; ++c)
         w[c] = (const uint16_t*)a.A + ((int64_t)adapter * a.R + min(c * 16 + l16, a.R - 1)) * a.K + grp * 8;
@@ -70,54 +168,66 @@ __device__ __forceinline__ void shrink(const LoraArgs& a, const int* list_s, int
     for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int c = 0; c < CT; ++c) acc[r][c] = v4f{0, 0, 0, 0};
-#pragma unroll 4
-    for (int s = s0; s < s1; ++s) {
-        const bool in = s * 32 + grp * 8 < a.K;              // K % 8 == 0: whole pieces
-        v4i xv[RT], wv[CT];
+    for (int u = u0; u < u1; ++u) {
+        const int k = u * kUnit;
+        v4i xv[kUnitSteps][RT], wv[kUnitSteps][CT];
+        if (k + kUnit <= a.K) {
 #pragma unroll
-        for (int r = 0; r < RT; ++r) xv[r] = in ? *(const v4i*)(x[r] + s * 32) : v4i{0, 0, 0, 0};
+            for (int s = 0; s < kUnitSteps; ++s) {
 #pragma unroll
-        for (int c = 0; c < CT; ++c) wv[c] = in ? *(const v4i*)(w[c] + s * 32) : v4i{0, 0, 0, 0};
+                for (int r = 0; r < RT; ++r) xv[s][r] = *(const v4i*)(x[r] + k + s * 32);
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
+                for (int c = 0; c < CT; ++c) wv[s][c] = *(const v4i*)(w[c] + k + s * 32);
+            }
+        } else {
 #pragma unroll
-            for (int c = 0; c < CT; ++c) acc[r][c] = mfma_bf16(xv[r], wv[c], acc[r][c]);
+            for (int s = 0; s < kUnitSteps; ++s) {
+                const bool in = k + s * 32 + grp * 8 < a.K;      // K % 8 == 0: whole pieces
+#pragma unroll
+                for (int r = 0; r < RT; ++r) xv[s][r] = in ? *(const v4i*)(x[r] + k + s * 32) : v4i{0, 0, 0, 0};
+#pragma unroll
+                for (int c = 0; c < CT; ++c) wv[s][c] = in ? *(const v4i*)(w[c] + k + s * 32) : v4i{0, 0, 0, 0};
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < kUnitSteps; ++s)
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int c = 0; c < CT; ++c) acc[r][c] = mfma_bf16(xv[s][r], wv[s][c], acc[r][c]);
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
+        if (r) __syncthreads();
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-            __syncthreads();
+        for (int c = 0; c < CT; ++c)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) sum_s[wave][grp * 4 + v][l16] = acc[r][c][v];
-            __syncthreads();
-            const int row = threadIdx.x >> 4, rank = c * 16 + (threadIdx.x & 15);
-            const float u = (sum_s[0][row][threadIdx.x & 15] + sum_s[1][row][threadIdx.x & 15]) +
-                            (sum_s[2][row][threadIdx.x & 15] + sum_s[3][row][threadIdx.x & 15]);
-            if (r * 16 + row < n && rank < a.R) {
-                const int64_t t = (int64_t)chunk * kLoraChunk + list_s[r * 16 + row];
-                a.U[((int64_t)split * a.T + t) * a.R + rank] = u;
-            }
+            for (int v = 0; v < 4; ++v) sum_s[wave][grp * 4 + v][c * 16 + l16] = acc[r][c][v];
+        __syncthreads();
+        for (int i = threadIdx.x; i < 16 * CT * 4; i += kThreads) {
+            const int row = i / (CT * 4), rank = i % (CT * 4) * 4;
+            if (r * 16 + row >= n || rank >= a.R) continue;      // R % 8 == 0
+            v4f s = *(const v4f*)&sum_s[0][row][rank];
+#pragma unroll
+            for (int m = 1; m < 4; ++m) s += *(const v4f*)&sum_s[m][row][rank];
+            *(v4f*)(a.U + ((int64_t)split * a.T + list_s[r * 16 + row]) * a.R + rank) = s;
         }
     }
     __syncthreads();
 }
 
-template <int CT>
+template <int CT, bool SORTED>
 __global__ __launch_bounds__(kThreads) void lora_shrink_kernel(LoraArgs a, int slots) {
-    __shared__ int list_s[kLoraChunk];
-    __shared__ float sum_s[4][16][16];
-    const int split = blockIdx.x % a.splits, slot = blockIdx.x / a.splits % slots, chunk = blockIdx.x / a.splits / slots;
-    ChunkRows at(a, chunk);
-    for (int i = 0; at.left; ++i) {
-        uint64_t rows;
-        const int adapter = at.next(rows);
-        if (i % slots != slot) continue;
-        const int n = __popcll(rows);
-        if (threadIdx.x < 64) list_rows(rows, list_s);
-        __syncthreads();
-        if (n <= 16) shrink<1, CT>(a, list_s, n, adapter, chunk, split, sum_s);
-        else shrink<kBlocks, CT>(a, list_s, n, adapter, chunk, split, sum_s);
+    __shared__ int list_s[kTile];
+    __shared__ __align__(16) float sum_s[4][16][CT * 16 + 4];
+    const int split = blockIdx.x % a.splits, slot = blockIdx.x / a.splits % slots, unit = blockIdx.x / a.splits / slots;
+    Tiles<SORTED> tiles(a, unit, slot, slots, false);
+    int adapter, n;
+    while (tiles.next(a, list_s, adapter, n)) {
+        if (SORTED && adapter < 0) break;                    // rows without an adapter come last
+        if (n <= 16) shrink<1, CT>(a, list_s, n, adapter, split, sum_s);
+        else if (n <= 32) shrink<2, CT>(a, list_s, n, adapter, split, sum_s);
+        else shrink<4, CT>(a, list_s, n, adapter, split, sum_s);
     }
 }
 
@@ -128,24 +238,18 @@ __global__ __launch_bounds__(kThreads) void lora_shrink_kernel(LoraArgs a, int s
 __device__ __forceinline__ void split_bf16(float u, uint16_t& hi, uint16_t& lo) {
     const __bf16 h = (__bf16)u;
     const float left = u - (float)h;
-    const __bf16 l = (__bf16)(left == left && fabsf(left) < __builtin_inff() ? left : 0.f);
+    const __bf16 l = (__bf16)(fabsf(left) < __builtin_inff() ? left : 0.f);
     hi = __builtin_bit_cast(uint16_t, h);
     lo = __builtin_bit_cast(uint16_t, l);
 }
 
-// A wave takes 64 columns of out for the rows of one adapter in a chunk.  D = B U^T:
-// a lane has one row of out and, with columns 16 (i / 4) + 4 b + i % 4 as row i of
-// block b, 16 consecutive columns of it.
+// A wave takes 64 columns of out for a tile.  D = B U^T: a lane has one row of out and,
+// with columns 16 (i / 4) + 4 b + i % 4 as row i of block b, 16 consecutive columns of
+// it.  Y and B are on their way while U's parts are added.
 template <int RT, int RS>
-__device__ __forceinline__ void expand(const LoraArgs& a, const int* list_s, const uint16_t (*u_s)[2][RS * 32 + 8], int n,
-                                       int adapter, int chunk, int col) {
+__device__ __forceinline__ void expand(const LoraArgs& a, const int* list_s, uint16_t (*u_s)[2][RS * 32 + 8], int n,
+                                       int adapter, int col) {
     const int lane = threadIdx.x & 63, l16 = lane & 15, grp = lane >> 4;
-    const float scale = a.scale ? a.scale[adapter] : 1.f;
-    v4f acc[RT][4];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) acc[r][b] = v4f{0, 0, 0, 0};
     v4i w[4][RS];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
@@ -159,23 +263,46 @@ __device__ __forceinline__ void expand(const LoraArgs& a, const int* list_s, con
     int64_t at[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-        at[r] = ((int64_t)chunk * kLoraChunk + list_s[min(r * 16 + l16, n - 1)]) * a.N + c;
+        at[r] = (int64_t)list_s[min(r * 16 + l16, n - 1)] * a.N + c;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             y[r][h] = c + 8 * h < a.N ? *(const u32x4*)((const uint16_t*)a.Y + at[r] + 8 * h) : u32x4{0, 0, 0, 0};
     }
+    const float scale = a.scale ? a.scale[adapter] : 1.f;
+    // U: four ranks a thread at a time, summed over the parts of K in order
+    for (int i = threadIdx.x; i < RT * 16 * RS * 8; i += kThreads) {
+        const int row = i / (RS * 8), rank = i % (RS * 8) * 4;
+        v4f u = {0, 0, 0, 0};
+        if (row < n && rank < a.R) {
+            const float* p = a.U + (int64_t)list_s[row] * a.R + rank;
+            const int64_t step = (int64_t)a.T * a.R;
+            int s = 0;
+            for (; s + 4 <= a.splits; s += 4) {
+                const v4f p0 = *(const v4f*)p, p1 = *(const v4f*)(p + step);
+                const v4f p2 = *(const v4f*)(p + 2 * step), p3 = *(const v4f*)(p + 3 * step);
+                u += (p0 + p1) + (p2 + p3);
+                p += 4 * step;
+            }
+            for (; s < a.splits; ++s, p += step) u += *(const v4f*)p;
+        }
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+        for (int j = 0; j < 4; ++j) split_bf16(u[j], u_s[row][0][rank + j], u_s[row][1][rank + j]);
+    }
+    lds_barrier();
+    if (col >= a.N) return;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        v4f acc[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) acc[b] = v4f{0, 0, 0, 0};
 #pragma unroll
         for (int s = 0; s < RS; ++s)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const v4i u = *(const v4i*)&u_s[r * 16 + l16][h][s * 32 + grp * 8];
+                const v4i u = lds_read_b128(&u_s[r * 16 + l16][h][s * 32 + grp * 8]);
 #pragma unroll
-                for (int b = 0; b < 4; ++b) acc[r][b] = mfma_bf16(w[b][s], u, acc[r][b]);
+                for (int b = 0; b < 4; ++b) acc[b] = mfma_bf16(w[b][s], u, acc[b]);
             }
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
         if (r * 16 + l16 >= n) continue;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -183,84 +310,76 @@ __device__ __forceinline__ void expand(const LoraArgs& a, const int* list_s, con
             float f[8];
             unpack8(y[r][h], f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = __builtin_fmaf(scale, acc[r][2 * h + j / 4][j % 4], f[j]);
+            for (int j = 0; j < 8; ++j) f[j] = __builtin_fmaf(scale, acc[2 * h + j / 4][j % 4], f[j]);
             *(u32x4*)((uint16_t*)a.out + at[r] + 8 * h) = pack8(f);
         }
     }
 }
 
-template <int RS>
+template <int RS, bool SORTED>
 __global__ __launch_bounds__(kThreads) void lora_expand_kernel(LoraArgs a, int slots, int panels) {
-    __shared__ int list_s[kLoraChunk];
-    __shared__ __align__(16) uint16_t u_s[kLoraChunk][2][RS * 32 + 8];   // 16 bytes more: rows on different banks
-    const int panel = blockIdx.x % panels, slot = blockIdx.x / panels % slots, chunk = blockIdx.x / panels / slots;
+    __shared__ int list_s[kTile];
+    __shared__ __align__(16) uint16_t u_s[kTile][2][RS * 32 + 8];        // 16 bytes more: rows on different banks
+    const int panel = blockIdx.x % panels, slot = blockIdx.x / panels % slots, unit = blockIdx.x / panels / slots;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int col = panel * 256 + wave * 64;
-    ChunkRows at(a, chunk);
-    const bool none = at.own < 0 && chunk * kLoraChunk + ((int)threadIdx.x & 63) < a.T;
-    const uint64_t bare = __ballot(none);                    // rows without an adapter
-    for (int i = 0; at.left; ++i) {
-        uint64_t rows;
-        const int adapter = at.next(rows);
-        if (i % slots != slot) continue;
-        const int n = __popcll(rows);
-        __syncthreads();
-        if (threadIdx.x < 64) list_rows(rows, list_s);
-        __syncthreads();
-        const int blocks = (n + 15) / 16;
-        for (int j = threadIdx.x; j < blocks * 16 * RS * 32; j += kThreads) {
-            const int row = j / (RS * 32), rank = j % (RS * 32);
-            float u = 0.f;
-            if (row < n && rank < a.R) {
-                const int64_t t = (int64_t)chunk * kLoraChunk + list_s[row];
-                for (int s = 0; s < a.splits; ++s) u += a.U[((int64_t)s * a.T + t) * a.R + rank];
+    Tiles<SORTED> tiles(a, unit, slot, slots, a.out != a.Y);
+    int adapter, n;
+    while (tiles.next(a, list_s, adapter, n)) {
+        if (adapter < 0) {                                   // copied: 32 lanes a row
+            const int c = panel * 256 + ((int)threadIdx.x & 31) * 8;
+            for (int i = threadIdx.x >> 5; i < n; i += kThreads / 32) {
+                const int64_t at = (int64_t)list_s[i] * a.N + c;
+                if (c < a.N) *(u32x4*)((uint16_t*)a.out + at) = *(const u32x4*)((const uint16_t*)a.Y + at);
             }
-            split_bf16(u, u_s[row][0][rank], u_s[row][1][rank]);
+        } else if (n <= 16) {
+            expand<1, RS>(a, list_s, u_s, n, adapter, col);
+        } else if (n <= 32) {
+            expand<2, RS>(a, list_s, u_s, n, adapter, col);
+        } else {
+            expand<4, RS>(a, list_s, u_s, n, adapter, col);
         }
         __syncthreads();
-        if (col < a.N) {
-            if (n <= 16) expand<1, RS>(a, list_s, u_s, n, adapter, chunk, col);
-            else expand<kBlocks, RS>(a, list_s, u_s, n, adapter, chunk, col);
-        }
     }
-    if (slot == 0 && a.out != a.Y)
-        for (uint64_t left = bare; left; left &= left - 1) {
-            const int64_t t = (int64_t)chunk * kLoraChunk + __builtin_ctzll(left);
-            const int c = panel * 256 + (int)threadIdx.x * 8;
-            if (threadIdx.x < 32 && c < a.N)
-                *(u32x4*)((uint16_t*)a.out + t * a.N + c) = *(const u32x4*)((const uint16_t*)a.Y + t * a.N + c);
-        }
 }
 
 // ----------------------------------------------------------------- launches
 
-// Workgroups that share a chunk's adapters among them: no more than there can be,
-// and no more than 1024 workgroups call for.
-static int lora_slots(const LoraArgs& a, int64_t others) {
-    int most = a.L < kLoraChunk ? a.L : kLoraChunk;
-    if (a.T < most) most = a.T;
-    const int64_t want = (1024 + others - 1) / others;
+// Workgroups that share the tiles of a chunk or window: no more than there can be
+// tiles, and no more than `goal` workgroups call for.
+static int lora_slots(int most, int64_t others, int goal) {
+    const int64_t want = (goal + others - 1) / others;
     return most < want ? most : (int)want;
+}
+
+template <int CT, int RS, bool SORTED>
+static hipError_t lora_as(const LoraArgs& a, hipStream_t s) {
+    const int64_t units = SORTED ? (a.T + kLoraWindow - 1) / kLoraWindow : (a.T + kLoraChunk - 1) / kLoraChunk;
+    const int panels = (a.N + 255) / 256;
+    int slots = lora_slots(a.max_tiles, units * a.splits, 2048);
+    lora_shrink_kernel<CT, SORTED><<<(unsigned)(units * slots * a.splits), kThreads, 0, s>>>(a, slots);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    slots = lora_slots(a.max_tiles, units * panels, 4096);
+    lora_expand_kernel<RS, SORTED><<<(unsigned)(units * slots * panels), kThreads, 0, s>>>(a, slots, panels);
+    return hipGetLastError();
+}
+
+template <bool SORTED>
+static hipError_t lora_with(const LoraArgs& a, hipStream_t s) {
+    if (a.R <= 16) return lora_as<1, 1, SORTED>(a, s);
+    if (a.R <= 32) return lora_as<2, 1, SORTED>(a, s);
+    if (a.R <= 64) return lora_as<4, 2, SORTED>(a, s);
+    return lora_as<8, 4, SORTED>(a, s);
 }
 
 hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
     if (a.T == 0) return hipSuccess;
-    const int64_t chunks = (a.T + kLoraChunk - 1) / kLoraChunk;
-    int slots = lora_slots(a, chunks * a.splits);
-    dim3 grid((unsigned)(chunks * slots * a.splits));
-    if (a.R <= 16) lora_shrink_kernel<1><<<grid, kThreads, 0, s>>>(a, slots);
-    else if (a.R <= 32) lora_shrink_kernel<2><<<grid, kThreads, 0, s>>>(a, slots);
-    else if (a.R <= 64) lora_shrink_kernel<4><<<grid, kThreads, 0, s>>>(a, slots);
-    else lora_shrink_kernel<8><<<grid, kThreads, 0, s>>>(a, slots);
+    if (!lora_sorted(a.T, a.L)) return lora_with<false>(a, s);
+    const unsigned windows = (unsigned)((a.T + kLoraWindow - 1) / kLoraWindow);
+    lora_sort_kernel<<<windows, 1024, (a.L + 1) * sizeof(int), s>>>(a, a.out != a.Y);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const int panels = (a.N + 255) / 256;
-    slots = lora_slots(a, chunks * panels);
-    grid = dim3((unsigned)(chunks * slots * panels));
-    if (a.R <= 32) lora_expand_kernel<1><<<grid, kThreads, 0, s>>>(a, slots, panels);
-    else if (a.R <= 64) lora_expand_kernel<2><<<grid, kThreads, 0, s>>>(a, slots, panels);
-    else lora_expand_kernel<4><<<grid, kThreads, 0, s>>>(a, slots, panels);
-    return hipGetLastError();
+    return e != hipSuccess ? e : lora_with<true>(a, s);
 }
 
 }  // namespace moegg

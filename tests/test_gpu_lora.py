@@ -1,8 +1,8 @@
 """Low-rank adapters on MI355X against the fp64 oracle (oracle/block.py).
 
 Bounds, with u = 2^-24 (half a step of fp32): products of two bf16 are exact in fp32.
-- U = X A^T: a wave's part of K is ceil(ceil(K / 32) / (4 splits)) steps of 32 products in one chain, then 4 waves and the
-  splits: c u of the terms' magnitudes.
+- U = X A^T: a wave's part of K is ceil(units / (4 splits)) units of 128 columns in one chain of products, then 4 waves
+  and the splits: c u of the terms' magnitudes.
 - U B^T: 2^-16 of U is lost in its two halves; 2 R products in a chain.
 - out: scale, Y's addition and two more roundings by u each, then bf16's 2^-8.
 """
@@ -58,9 +58,10 @@ def reference(i, scale=True):
     R, L = A.shape[1], A.shape[0]
     who = i["adapter"].numpy()
     ref, err = Y.copy(), np.zeros_like(Y)
-    chunks = (T + 63) // 64
-    splits = min((K + 511) // 512, (512 + chunks - 1) // chunks)
-    chain = (-(-(-(-K // 32)) // (4 * splits)) * 32 + 4 + splits) * U
+    tiles, units = (T + 63) // 64, (K + 127) // 128
+    each = -(-units // (4 * -(-512 // tiles)))
+    splits = -(-units // (4 * each))
+    chain = (each * 128 + 4 + splits) * U
     for a in range(L):
         rows = np.nonzero(who == a)[0]
         if len(rows) == 0:
@@ -95,6 +96,21 @@ def test_rows_in_any_order(T, K, N, R, L):
     check(i, scale=False, in_place=True)
 
 
+@pytest.mark.parametrize("T,K,N,R,L", [(256, 64, 64, 8, 7), (257, 64, 72, 16, 300), (1000, 128, 264, 32, 1), (4096, 72, 40, 64, 64),
+                                       (8192, 40, 8, 8, 1500), (8193, 64, 48, 16, 3), (16500, 32, 24, 128, 9000),
+                                       (500, 64, 64, 16, 16383), (500, 64, 64, 16, 16384), (500, 64, 64, 16, 20000)])
+def test_many_rows_in_any_order(T, K, N, R, L):
+    """Rows sorted by adapter, window by window, or (too many adapters to count) taken as they come."""
+    print("CASE lora many", T, K, N, R, L, flush=True)
+    i = inputs(T, K, N, R, L, T + L)
+    check(i)
+    i["adapter"][i["adapter"] % 2 == 0] = -1
+    check(i, in_place=True)
+    check(i, scale=False)
+    i["adapter"][:] = L - 1
+    check(i)
+
+
 @pytest.mark.parametrize("T,K,N,R,L,longest", [(64, 256, 256, 16, 2, 64), (500, 512, 384, 16, 4, 300),
                                                (1000, 320, 512, 64, 9, 40), (4100, 128, 264, 8, 5, 3000),
                                                (257, 1024, 640, 32, 3, 17)])
@@ -126,7 +142,11 @@ def test_whole_numbers_are_exact():
 
 
 def test_rows_without_an_adapter():
-    i = inputs(150, 64, 128, 16, 3, 5)
+    for T in (150, 600):
+        _without_an_adapter(inputs(T, 64, 128, 16, 3, 5))
+
+
+def _without_an_adapter(i):
     i["adapter"][:] = -1
     i["X"][:] = float("nan")                                 # not looked at
     assert torch.equal(run(i).cpu().view(torch.int16), i["Y"].view(torch.int16))
@@ -135,15 +155,16 @@ def test_rows_without_an_adapter():
     assert torch.equal(run(i, in_place=True).cpu().view(torch.int16), i["Y"].view(torch.int16))
 
 
-def test_nan_and_infinities_stay_in_their_rows_and_adapters():
-    i = inputs(130, 256, 64, 16, 4, 6)
-    i["adapter"] = torch.arange(130, dtype=I32) % 4
+@pytest.mark.parametrize("T", [130, 390])
+def test_nan_and_infinities_stay_in_their_rows_and_adapters(T):
+    i = inputs(T, 256, 64, 16, 4, 6)
+    i["adapter"] = torch.arange(T, dtype=I32) % 4
     j = {n: v.clone() for n, v in i.items()}
     j["X"][5, 7], j["X"][70, 3] = float("nan"), float("inf")
     j["A"][2, 3] = float("nan")
     j["B"][3, 11] = float("inf")
     a, b = f64(run(i)), f64(run(j))
-    hit = np.zeros((130, 64), dtype=bool)
+    hit = np.zeros((T, 64), dtype=bool)
     hit[[5, 70]] = True
     hit[2::4] = True
     hit[3::4, 11] = True
@@ -151,8 +172,8 @@ def test_nan_and_infinities_stay_in_their_rows_and_adapters():
     assert not np.isfinite(b[70]).any() and not np.isfinite(b[3::4, 11]).any()
 
 
-def test_nothing_is_written_past_the_outputs():
-    T, K, N, R, L = 77, 72, 88, 24, 5
+@pytest.mark.parametrize("T,K,N,R,L", [(77, 72, 88, 24, 5), (300, 72, 88, 24, 5), (8500, 136, 8, 8, 7000)])
+def test_nothing_is_written_past_the_outputs(T, K, N, R, L):
     i = inputs(T, K, N, R, L, 7)
     n = mg.lora_workspace_bytes(T, K, R)
     ws = torch.full((n + 512,), SENTINEL, dtype=torch.uint8, device="cuda")
@@ -170,9 +191,10 @@ def test_no_rows():
 
 
 def test_a_larger_workspace_and_repeated_bits():
-    i = inputs(200, 1536, 256, 16, 6, 9)
-    a = run(i)
-    assert torch.equal(a, run(i, ws=mg.lora_workspace(5000, 1536, 16))) and torch.equal(a, run(i))
+    for T in (200, 2000):
+        i = inputs(T, 1536, 256, 16, 6, 9)
+        a = run(i)
+        assert torch.equal(a, run(i, ws=mg.lora_workspace(5000, 1536, 16))) and torch.equal(a, run(i))
 
 
 def test_weights_past_32_bit_offsets():
@@ -194,8 +216,9 @@ def test_weights_past_32_bit_offsets():
     assert (np.abs(f64(out) - ref) <= err).all()
 
 
-def test_graph_and_stream():
-    T, K, N, R, L = 140, 512, 256, 16, 6
+@pytest.mark.parametrize("T", [140, 1400])
+def test_graph_and_stream(T):
+    K, N, R, L = 512, 256, 16, 6
     d = {n: v.cuda() for n, v in inputs(T, K, N, R, L, 1).items()}
     out, ws = torch.empty(T, N, dtype=BF16, device="cuda"), mg.lora_workspace(T, K, R)
 
