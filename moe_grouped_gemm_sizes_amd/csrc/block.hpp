@@ -75,7 +75,7 @@ struct LoraArgs {
     float* U;                            // [splits, T, R]
     int32_t* order;                      // [T]: rows by adapter, window by window
     int4* tiles;                         // [windows, max_tiles]: adapter, first place in `order`, rows
-    int32_t* n_tiles;                    // [windows]
+                                         // (0 past the last one)
     int T, K, N, R, L;
     int splits;                          // of K
     int max_tiles;                       // of a window, or of a chunk
@@ -105,14 +105,23 @@ inline bool lora_sorted(int T, int L) { return T > kLoraChunkRows && L < kLoraMa
 inline int lora_max_tiles(int T, int L) {
     const bool sorted = lora_sorted(T, L);
     const int most = sorted ? kLoraWindow : kLoraChunk, rows = T < most ? T : most;
-    return (sorted ? rows / kLoraChunk : 0) + (L < rows ? L + 1 : rows);
+    const int all = rows / (sorted ? kLoraChunk : 16) + (L < rows ? L + 1 : rows);
+    return sorted || all < rows ? all : rows;
+}
+
+// Entries of the tile lists of any call of up to T rows.
+inline int64_t lora_tile_slots(int T) {
+    const int64_t windows = ((int64_t)T + kLoraWindow - 1) / kLoraWindow, rows = T < kLoraWindow ? T : kLoraWindow;
+    return windows * (rows / kLoraChunk + rows);
 }
 
 // Parts of K that workgroups of the first product take: 2 units of 128 columns a wave (1 where
-// rows are few), and no more of them than make 512 workgroups of full tiles.
-inline int lora_splits(int T, int K) {
-    const int tiles = (T + kLoraChunk - 1) / kLoraChunk, units = (K + 127) / 128;
-    const int want = tiles > 0 ? (512 + tiles - 1) / tiles : 1;
+// rows are few), and no more of them than make 512 workgroups of full tiles, or 256 past a rank of
+// 32, whose sums are more to add (8191 rows, 2048 -> 64 -> 7168: 512 92 us, 256 86 us; 4096 rows,
+// 7168 -> 16 -> 4096: 40 and 42 us, 1024 44 us).
+inline int lora_splits(int T, int K, int R) {
+    const int tiles = (T + kLoraChunk - 1) / kLoraChunk, units = (K + 127) / 128, most = R <= 32 ? 512 : 256;
+    const int want = tiles > 0 ? (most + tiles - 1) / tiles : 1;
     const int each = (units + 4 * want - 1) / (4 * want);
     return (units + 4 * each - 1) / (4 * each);
 }

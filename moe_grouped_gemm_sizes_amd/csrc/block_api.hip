@@ -41,19 +41,16 @@ size_t balance_pieces(int T, int S) { return std::min<size_t>(((size_t)T + 31) /
 
 // Workspace of the adapters' call, which serves every call of fewer rows.
 struct LoraLayout {
-    size_t order, tiles, n_tiles, total;
+    size_t order, tiles, total;
 };
 LoraLayout lora_layout(int T, int K, int R) {
-    // parts of K times rows: those of 512 full tiles, or T; and no more than a part for 4 units and row
+    // parts of K times rows: those of 512 workgroups' tiles, or T; and no more parts than there is work for
     const size_t units = ((size_t)K + 127) / 128, rows = T;
     const size_t parts = std::max(std::min(rows * ((units + 3) / 4), (size_t)1024 * kLoraChunk), rows);
-    const size_t windows = (rows + kLoraWindow - 1) / kLoraWindow;
     LoraLayout l;
     l.order = align256(parts * sizeof(float) * (size_t)R);
     l.tiles = l.order + align256(rows * sizeof(int32_t));
-    // a window's tiles: of one row each, and full ones
-    l.n_tiles = l.tiles + align256((rows + rows / kLoraChunk) * sizeof(int4));
-    l.total = l.n_tiles + align256(std::max<size_t>(windows, 1) * sizeof(int32_t));
+    l.total = l.tiles + align256(std::max<size_t>(lora_tile_slots(T), 1) * sizeof(int4));
     return l;
 }
 
@@ -210,13 +207,12 @@ moegg_status_t moegg_lora(const void* X, const void* A, const void* B, const flo
     a.U = (float*)w;
     a.order = (int32_t*)(w + at.order);
     a.tiles = (int4*)(w + at.tiles);
-    a.n_tiles = (int32_t*)(w + at.n_tiles);
     a.T = T;
     a.K = K;
     a.N = N;
     a.R = R;
     a.L = L;
-    a.splits = lora_splits(T, K);
+    a.splits = lora_splits(T, K, R);
     a.max_tiles = lora_max_tiles(T, L);
     return hip_status(launch_lora(a, (hipStream_t)stream), "low-rank adapters");
 }

@@ -2,11 +2,11 @@
 //     out[t] = Y[t] + scale_a (X[t] A_a^T) B_a^T,   a the adapter of row t.
 //
 // Two products with a rank of 8 to 128, so that rows and weights are moved and little
-// is computed.  Both take tiles: up to 64 rows with one adapter.  Up to 256 rows the
-// kernels find these by themselves: a wave looks at 64 consecutive rows, a lane
-// each, and takes the adapters among them one by one.  Beyond, a first launch
-// sorts windows of 8192 rows by their adapters, so that an adapter's weights are read
-// for 64 rows together whatever the order of the rows.
+// is computed.  Both take tiles of rows with one adapter.  Up to 256 rows the kernels
+// find these by themselves: a wave looks at 64 consecutive rows, a lane each, and
+// takes the adapters among them one by one, up to 16 rows a tile.  Beyond, a first
+// launch sorts windows of 8192 rows by their adapters, so that an adapter's weights
+// are read for 64 rows together whatever the order of the rows.
 #include <hip/hip_runtime.h>
 
 #include "block.hpp"
@@ -16,8 +16,13 @@
 
 namespace moegg {
 
-constexpr int kThreads = 256;
+#ifndef ET
+#define ET 256
+#endif
+constexpr int kThreads = 256;             // of the first product
+constexpr int kExpandThreads = ET;       // of the second: as many columns of out
 constexpr int kTile = kLoraChunk;         // rows of a tile
+constexpr int kChunkTile = 16;            // and of one that was not sorted
 
 // ----------------------------------------------------------------- tiles
 
@@ -85,8 +90,9 @@ __global__ __launch_bounds__(1024) void lora_sort_kernel(LoraArgs a, int copy) {
             for (int b = 0; b < c; b += kTile) tiles[tile++] = int4{k < a.L ? k : -1, first + place + b, min(kTile, c - b), 0};
         place += c;
     }
-    if (threadIdx.x == 1023) a.n_tiles[blockIdx.x] = tile;
+    if (threadIdx.x == 1023) tiles_s[0] = tile;
     __syncthreads();
+    for (int i = tiles_s[0] + (int)threadIdx.x; i < a.max_tiles; i += 1024) tiles[i] = int4{-1, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
         if (key[i] >= 0) a.order[first + count_s[key[i]] + rank[i]] = first + i * 1024 + (int)threadIdx.x;
@@ -98,12 +104,10 @@ template <bool SORTED>
 struct Tiles {
     int own;                             // chunk: this lane's adapter, -1: none or past the last row
     uint64_t left;                       // chunk: rows not taken yet
-    int at, end, slots, unit;
+    int at, slots, unit;
     __device__ __forceinline__ Tiles(const LoraArgs& a, int unit_, int slot, int slots_, bool bare)
         : at(slot), slots(slots_), unit(unit_) {
-        if (SORTED) {
-            end = a.n_tiles[unit];
-        } else {
+        if (!SORTED) {
             const int t = unit * kLoraChunk + ((int)threadIdx.x & 63);
             own = t < a.T ? a.adapter[t] : -2;
             if (own != -2) own = (uint32_t)own < (uint32_t)a.L ? own : -1;
@@ -111,9 +115,14 @@ struct Tiles {
             for (int i = 0; i < slot && left; ++i) take();
         }
     }
+    // The rows of the next tile: the first 16 of the next adapter's.
     __device__ __forceinline__ uint64_t take() {
         const int first = __builtin_amdgcn_readlane(own, __builtin_ctzll(left));
-        const uint64_t rows = __ballot(own == first);
+        uint64_t rows = __ballot(own == first) & left;
+        if (__popcll(rows) > kChunkTile) {
+            const int lane = threadIdx.x & 63;
+            rows = __ballot((rows >> lane & 1) && __popcll(rows & ((1ull << lane) - 1)) < kChunkTile);
+        }
         left &= ~rows;
         return rows;
     }
@@ -121,10 +130,11 @@ struct Tiles {
     __device__ __forceinline__ bool next(const LoraArgs& a, int* list_s, int& adapter, int& n) {
         const int lane = threadIdx.x & 63;
         if (SORTED) {
-            if (at >= end) return false;
+            if (at >= a.max_tiles) return false;
             const int4 tile = a.tiles[(int64_t)unit * a.max_tiles + at];
             adapter = __builtin_amdgcn_readfirstlane(tile.x);
             n = __builtin_amdgcn_readfirstlane(tile.z);
+            if (n == 0) return false;
             if (threadIdx.x < 64) list_s[lane] = a.order[tile.y + min(lane, n - 1)];
             at += slots;
         } else {
@@ -143,14 +153,15 @@ struct Tiles {
 
 // ----------------------------------------------------------------- X A^T
 
-// A workgroup takes a tile and a part of K, its waves a quarter of that each; their
+// A workgroup takes a tile and a part of K, its waves a share of that each; their
 // sums meet in LDS.  D = X A^T in blocks of 16 rows x 16 ranks.  K goes in units of 128
 // columns, whole lines, all of whose loads are in flight together.
-constexpr int kUnit = 128, kUnitSteps = kUnit / 32;
+constexpr int kUnit = 128;
 
 template <int RT, int CT>
 __device__ __forceinline__ void shrink(const LoraArgs& a, const int* list_s, int n, int adapter, int split,
                                        float (*sum_s)[16][CT * 16 + 4]) {
+    constexpr int kSteps = CT <= 2 ? kUnit / 32 : kUnit / 64;    // loaded together; higher ranks: half a unit
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int l16 = lane & 15, grp = lane >> 4;
     const int units = (a.K + kUnit - 1) / kUnit, shares = a.splits * 4, share = split * 4 + wave;
@@ -168,12 +179,11 @@ __device__ __forceinline__ void shrink(const LoraArgs& a, const int* list_s, int
     for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int c = 0; c < CT; ++c) acc[r][c] = v4f{0, 0, 0, 0};
-    for (int u = u0; u < u1; ++u) {
-        const int k = u * kUnit;
-        v4i xv[kUnitSteps][RT], wv[kUnitSteps][CT];
-        if (k + kUnit <= a.K) {
+    for (int k = u0 * kUnit; k < u1 * kUnit; k += kSteps * 32) {
+        v4i xv[kSteps][RT], wv[kSteps][CT];
+        if (k + kSteps * 32 <= a.K) {
 #pragma unroll
-            for (int s = 0; s < kUnitSteps; ++s) {
+            for (int s = 0; s < kSteps; ++s) {
 #pragma unroll
                 for (int r = 0; r < RT; ++r) xv[s][r] = *(const v4i*)(x[r] + k + s * 32);
 #pragma unroll
@@ -181,7 +191,7 @@ __device__ __forceinline__ void shrink(const LoraArgs& a, const int* list_s, int
             }
         } else {
 #pragma unroll
-            for (int s = 0; s < kUnitSteps; ++s) {
+            for (int s = 0; s < kSteps; ++s) {
                 const bool in = k + s * 32 + grp * 8 < a.K;      // K % 8 == 0: whole pieces
 #pragma unroll
                 for (int r = 0; r < RT; ++r) xv[s][r] = in ? *(const v4i*)(x[r] + k + s * 32) : v4i{0, 0, 0, 0};
@@ -189,8 +199,9 @@ __device__ __forceinline__ void shrink(const LoraArgs& a, const int* list_s, int
                 for (int c = 0; c < CT; ++c) wv[s][c] = in ? *(const v4i*)(w[c] + k + s * 32) : v4i{0, 0, 0, 0};
             }
         }
+        __builtin_amdgcn_sched_barrier(0);                       // no product before the last load is sent
 #pragma unroll
-        for (int s = 0; s < kUnitSteps; ++s)
+        for (int s = 0; s < kSteps; ++s)
 #pragma unroll
             for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -225,7 +236,7 @@ __global__ __launch_bounds__(kThreads) void lora_shrink_kernel(LoraArgs a, int s
     int adapter, n;
     while (tiles.next(a, list_s, adapter, n)) {
         if (SORTED && adapter < 0) break;                    // rows without an adapter come last
-        if (n <= 16) shrink<1, CT>(a, list_s, n, adapter, split, sum_s);
+        if (!SORTED || n <= 16) shrink<1, CT>(a, list_s, n, adapter, split, sum_s);
         else if (n <= 32) shrink<2, CT>(a, list_s, n, adapter, split, sum_s);
         else shrink<4, CT>(a, list_s, n, adapter, split, sum_s);
     }
@@ -243,50 +254,84 @@ __device__ __forceinline__ void split_bf16(float u, uint16_t& hi, uint16_t& lo) 
     lo = __builtin_bit_cast(uint16_t, l);
 }
 
-// A wave takes 64 columns of out for a tile.  D = B U^T: a lane has one row of out and,
-// with columns 16 (i / 4) + 4 b + i % 4 as row i of block b, 16 consecutive columns of
-// it.  Y and B are on their way while U's parts are added.
+// A wave takes 64 columns of out at a time for a tile.  D = B U^T: a lane has one row of out
+// and, with columns 32 (b / 2) + 8 (i / 4) + 4 (b % 2) + i % 4 as row i of block b, twice 8
+// consecutive columns of it.  Neighbouring lanes exchange one of the two, so that a load
+// or store moves 8 rows of 128 bytes, whole lines, and not halves of 16.
+__device__ __forceinline__ void swap_halves(u32x4& first, u32x4& second) {
+    const bool odd = threadIdx.x & 1;
+    const u32x4 send = odd ? first : second;
+    const u32x4 got = {lane_of<DPP_XOR1>(send.x), lane_of<DPP_XOR1>(send.y), lane_of<DPP_XOR1>(send.z),
+                       lane_of<DPP_XOR1>(send.w)};
+    if (odd) first = got;
+    else second = got;
+}
+// Y and B are on their way while U's parts are added.
 template <int RT, int RS>
-__device__ __forceinline__ void expand(const LoraArgs& a, const int* list_s, uint16_t (*u_s)[2][RS * 32 + 8], int n,
+__device__ __forceinline__ void expand(const LoraArgs& a, const int* list_s, uint16_t (*u_s)[RS * 64 + 8], int n,
                                        int adapter, int col) {
     const int lane = threadIdx.x & 63, l16 = lane & 15, grp = lane >> 4;
+    // U: four ranks a thread at a time, summed over the parts of K in order.  Loads return in the
+    // order in which they were sent: the last of U's go before those of Y and B.
+    constexpr int kItems = RT * 16 * RS * 8, kEach = (kItems + kExpandThreads - 1) / kExpandThreads;
+    constexpr int kParts = RT == 1 ? 8 : (RT == 2 ? 4 : 2);      // loaded together
+    v4f u[kEach], p[kParts][kEach];
+    const int64_t step = (int64_t)a.T * a.R;
+    auto part = [&](int j, int s) {
+        const int i = j * kExpandThreads + (int)threadIdx.x, row = i / (RS * 8), rank = i % (RS * 8) * 4;
+        return row < n && rank < a.R && s < a.splits ? *(const v4f*)(a.U + s * step + (int64_t)list_s[row] * a.R + rank)
+                                                    : v4f{0, 0, 0, 0};
+    };
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) u[j] = v4f{0, 0, 0, 0};
+    int s0 = 0;
+    auto parts = [&]() {
+#pragma unroll
+        for (int s = 0; s < kParts; ++s)
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) p[s][j] = part(j, s0 + s);
+    };
+    auto add = [&]() {
+#pragma unroll
+        for (int s = 0; s < kParts; ++s)
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) u[j] += p[s][j];
+    };
+    for (; s0 + kParts < a.splits; s0 += kParts) {
+        parts();
+        add();
+    }
+    parts();
+    __builtin_amdgcn_sched_barrier(0);
     v4i w[4][RS];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-        const int c = col + 16 * (l16 >> 2) + 4 * b + (l16 & 3);
+        const int c = col + 32 * (b >> 1) + 8 * (l16 >> 2) + 4 * (b & 1) + (l16 & 3);
         const uint16_t* p = (const uint16_t*)a.B + ((int64_t)adapter * a.N + min(c, a.N - 1)) * a.R + grp * 8;
 #pragma unroll
         for (int s = 0; s < RS; ++s) w[b][s] = s * 32 + grp * 8 < a.R ? *(const v4i*)(p + s * 32) : v4i{0, 0, 0, 0};
     }
-    const int c = col + 16 * grp;                            // this lane's 16 columns
+    // the lane's place in its i-th access to row block r: of an even row, or of the odd one after it
+    const int c = col + 8 * grp + 32 * (l16 & 1);            // N % 8 == 0: whole pieces
+    auto place = [&](int r, int i) { return (int64_t)list_s[min(r * 16 + (l16 & 14) + i, n - 1)] * a.N + c; };
     u32x4 y[RT][2];
-    int64_t at[RT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        at[r] = (int64_t)list_s[min(r * 16 + l16, n - 1)] * a.N + c;
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            y[r][h] = c + 8 * h < a.N ? *(const u32x4*)((const uint16_t*)a.Y + at[r] + 8 * h) : u32x4{0, 0, 0, 0};
-    }
+        for (int i = 0; i < 2; ++i)
+            y[r][i] = c < a.N ? *(const u32x4*)((const uint16_t*)a.Y + place(r, i)) : u32x4{0, 0, 0, 0};
     const float scale = a.scale ? a.scale[adapter] : 1.f;
-    // U: four ranks a thread at a time, summed over the parts of K in order
-    for (int i = threadIdx.x; i < RT * 16 * RS * 8; i += kThreads) {
-        const int row = i / (RS * 8), rank = i % (RS * 8) * 4;
-        v4f u = {0, 0, 0, 0};
-        if (row < n && rank < a.R) {
-            const float* p = a.U + (int64_t)list_s[row] * a.R + rank;
-            const int64_t step = (int64_t)a.T * a.R;
-            int s = 0;
-            for (; s + 4 <= a.splits; s += 4) {
-                const v4f p0 = *(const v4f*)p, p1 = *(const v4f*)(p + step);
-                const v4f p2 = *(const v4f*)(p + 2 * step), p3 = *(const v4f*)(p + 3 * step);
-                u += (p0 + p1) + (p2 + p3);
-                p += 4 * step;
-            }
-            for (; s < a.splits; ++s, p += step) u += *(const v4f*)p;
-        }
+    __builtin_amdgcn_sched_barrier(0);
+    add();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) split_bf16(u[j], u_s[row][0][rank + j], u_s[row][1][rank + j]);
+    for (int j = 0; j < kEach; ++j) {
+        const int i = j * kExpandThreads + (int)threadIdx.x, row = i / (RS * 8), rank = i % (RS * 8) * 4;
+        if (i >= kItems) break;
+        uint16_t hi[4], lo[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) split_bf16(u[j][m], hi[m], lo[m]);
+        *(u32x2*)&u_s[row][rank] = u32x2{hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16};
+        *(u32x2*)&u_s[row][RS * 32 + rank] = u32x2{lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16};
     }
     lds_barrier();
     if (col >= a.N) return;
@@ -299,45 +344,50 @@ __device__ __forceinline__ void expand(const LoraArgs& a, const int* list_s, uin
         for (int s = 0; s < RS; ++s)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const v4i u = lds_read_b128(&u_s[r * 16 + l16][h][s * 32 + grp * 8]);
+                const v4i u = lds_read_b128(&u_s[r * 16 + l16][(h * RS + s) * 32 + grp * 8]);
 #pragma unroll
                 for (int b = 0; b < 4; ++b) acc[b] = mfma_bf16(w[b][s], u, acc[b]);
             }
-        if (r * 16 + l16 >= n) continue;
+        swap_halves(y[r][0], y[r][1]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            if (c + 8 * h >= a.N) continue;                  // N % 8 == 0
             float f[8];
             unpack8(y[r][h], f);
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] = __builtin_fmaf(scale, acc[2 * h + j / 4][j % 4], f[j]);
-            *(u32x4*)((uint16_t*)a.out + at[r] + 8 * h) = pack8(f);
+            y[r][h] = pack8(f);
         }
+        swap_halves(y[r][0], y[r][1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (r * 16 + (l16 & 14) + i < n && c < a.N) store_once((uint16_t*)a.out + place(r, i), y[r][i]);
     }
 }
 
+#ifndef EB
+#define EB 2
+#endif
 template <int RS, bool SORTED>
-__global__ __launch_bounds__(kThreads) void lora_expand_kernel(LoraArgs a, int slots, int panels) {
+__global__ __launch_bounds__(kExpandThreads, EB) void lora_expand_kernel(LoraArgs a, int slots, int panels) {
     __shared__ int list_s[kTile];
-    __shared__ __align__(16) uint16_t u_s[kTile][2][RS * 32 + 8];        // 16 bytes more: rows on different banks
+    __shared__ __align__(16) uint16_t u_s[kTile][RS * 64 + 8];   // 16 bytes more: 16 rows' pieces on all banks
     const int panel = blockIdx.x % panels, slot = blockIdx.x / panels % slots, unit = blockIdx.x / panels / slots;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int col = panel * 256 + wave * 64;
     Tiles<SORTED> tiles(a, unit, slot, slots, a.out != a.Y);
     int adapter, n;
     while (tiles.next(a, list_s, adapter, n)) {
-        if (adapter < 0) {                                   // copied: 32 lanes a row
-            const int c = panel * 256 + ((int)threadIdx.x & 31) * 8;
-            for (int i = threadIdx.x >> 5; i < n; i += kThreads / 32) {
+        if (adapter < 0) {                                   // copied: 8 columns a thread, 8 rows together
+            const int c = panel * kExpandThreads + (int)threadIdx.x % (kExpandThreads / 8) * 8;
+            for (int i = (int)threadIdx.x / (kExpandThreads / 8); i < n; i += 8) {
                 const int64_t at = (int64_t)list_s[i] * a.N + c;
                 if (c < a.N) *(u32x4*)((uint16_t*)a.out + at) = *(const u32x4*)((const uint16_t*)a.Y + at);
             }
-        } else if (n <= 16) {
-            expand<1, RS>(a, list_s, u_s, n, adapter, col);
+        } else if (!SORTED || n <= 16) {
+            expand<1, RS>(a, list_s, u_s, n, adapter, panel * kExpandThreads + wave * 64);
         } else if (n <= 32) {
-            expand<2, RS>(a, list_s, u_s, n, adapter, col);
+            expand<2, RS>(a, list_s, u_s, n, adapter, panel * kExpandThreads + wave * 64);
         } else {
-            expand<4, RS>(a, list_s, u_s, n, adapter, col);
+            expand<4, RS>(a, list_s, u_s, n, adapter, panel * kExpandThreads + wave * 64);
         }
         __syncthreads();
     }
@@ -355,13 +405,13 @@ static int lora_slots(int most, int64_t others, int goal) {
 template <int CT, int RS, bool SORTED>
 static hipError_t lora_as(const LoraArgs& a, hipStream_t s) {
     const int64_t units = SORTED ? (a.T + kLoraWindow - 1) / kLoraWindow : (a.T + kLoraChunk - 1) / kLoraChunk;
-    const int panels = (a.N + 255) / 256;
+    const int panels = (a.N + kExpandThreads - 1) / kExpandThreads;
     int slots = lora_slots(a.max_tiles, units * a.splits, 2048);
     lora_shrink_kernel<CT, SORTED><<<(unsigned)(units * slots * a.splits), kThreads, 0, s>>>(a, slots);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     slots = lora_slots(a.max_tiles, units * panels, 4096);
-    lora_expand_kernel<RS, SORTED><<<(unsigned)(units * slots * panels), kThreads, 0, s>>>(a, slots, panels);
+    lora_expand_kernel<RS, SORTED><<<(unsigned)(units * slots * panels), kExpandThreads, 0, s>>>(a, slots, panels);
     return hipGetLastError();
 }
 

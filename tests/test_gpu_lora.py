@@ -1,8 +1,8 @@
 """Low-rank adapters on MI355X against the fp64 oracle (oracle/block.py).
 
 Bounds, with u = 2^-24 (half a step of fp32): products of two bf16 are exact in fp32.
-- U = X A^T: a wave's part of K is ceil(units / (4 splits)) units of 128 columns in one chain of products, then 4 waves
-  and the splits: c u of the terms' magnitudes.
+- U = X A^T: a wave's part of K is up to ceil(units / (4 splits)) units of 128 columns in one chain of products, then 4
+  waves and the splits: c u of the terms' magnitudes.
 - U B^T: 2^-16 of U is lost in its two halves; 2 R products in a chain.
 - out: scale, Y's addition and two more roundings by u each, then bf16's 2^-8.
 """
@@ -59,7 +59,7 @@ def reference(i, scale=True):
     who = i["adapter"].numpy()
     ref, err = Y.copy(), np.zeros_like(Y)
     tiles, units = (T + 63) // 64, (K + 127) // 128
-    each = -(-units // (4 * -(-512 // tiles)))
+    each = -(-units // (4 * -(-(512 if R <= 32 else 256) // tiles)))
     splits = -(-units // (4 * each))
     chain = (each * 128 + 4 + splits) * U
     for a in range(L):
