@@ -118,12 +118,14 @@ inline int64_t lora_tile_slots(int T) {
 // Parts of K that workgroups of the first product take: 2 units of 128 columns a wave (1 where
 // rows are few), and no more of them than make 512 workgroups of full tiles, or 256 past a rank of
 // 32, whose sums are more to add (8191 rows, 2048 -> 64 -> 7168: 512 92 us, 256 86 us; 4096 rows,
-// 7168 -> 16 -> 4096: 40 and 42 us, 1024 44 us).
+// 7168 -> 16 -> 4096: 40 and 42 us, 1024 44 us).  Rows in chunks are taken to share an adapter in
+// pairs (96 rows, 64 adapters: 18.1 us; all 64 alike 18.6 us, none 18.4 us).
 inline int lora_splits(int T, int K, int R) {
-    const int tiles = (T + kLoraChunk - 1) / kLoraChunk, units = (K + 127) / 128, most = R <= 32 ? 512 : 256;
+    const int each = T <= kLoraChunkRows ? 2 : kLoraChunk, most = R <= 32 ? 512 : 256;
+    const int tiles = (T + each - 1) / each, units = (K + 127) / 128;
     const int want = tiles > 0 ? (most + tiles - 1) / tiles : 1;
-    const int each = (units + 4 * want - 1) / (4 * want);
-    return (units + 4 * each - 1) / (4 * each);
+    const int share = (units + 4 * want - 1) / (4 * want);
+    return (units + 4 * share - 1) / (4 * share);
 }
 
 }  // namespace moegg

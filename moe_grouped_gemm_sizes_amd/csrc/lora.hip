@@ -102,29 +102,25 @@ __global__ __launch_bounds__(1024) void lora_sort_kernel(LoraArgs a, int copy) {
 // their rows listed in LDS.
 template <bool SORTED>
 struct Tiles {
-    int own;                             // chunk: this lane's adapter, -1: none or past the last row
-    uint64_t left;                       // chunk: rows not taken yet
     int at, slots, unit;
+    int own, rank;                       // chunk: this lane's adapter (-1: none, -2: no row), earlier rows with the same
+    uint64_t starts;                     // chunk: first rows of tiles
+
+    // A row starts a tile if the number of earlier rows with its adapter is a multiple of
+    // 16: counted for all rows at once, one comparison with each row.  Taking adapter
+    // after adapter instead costs a late tile of 40 adapters 1 us.
     __device__ __forceinline__ Tiles(const LoraArgs& a, int unit_, int slot, int slots_, bool bare)
         : at(slot), slots(slots_), unit(unit_) {
         if (!SORTED) {
-            const int t = unit * kLoraChunk + ((int)threadIdx.x & 63);
-            own = t < a.T ? a.adapter[t] : -2;
-            if (own != -2) own = (uint32_t)own < (uint32_t)a.L ? own : -1;
-            left = __ballot(own >= 0 || (bare && own == -1));
-            for (int i = 0; i < slot && left; ++i) take();
+            const int lane = threadIdx.x & 63, first = unit * kLoraChunk, rows = min(a.T - first, kLoraChunk);
+            own = lane < rows ? a.adapter[first + lane] : -2;
+            if (lane < rows) own = (uint32_t)own < (uint32_t)a.L ? own : -1;
+            rank = 0;
+            for (int i = 0; i < rows; i += 8)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) rank += (__builtin_amdgcn_readlane(own, i + j) == own) & (i + j < lane);
+            starts = __ballot(rank % kChunkTile == 0 && (own >= 0 || (bare && own == -1)));
         }
-    }
-    // The rows of the next tile: the first 16 of the next adapter's.
-    __device__ __forceinline__ uint64_t take() {
-        const int first = __builtin_amdgcn_readlane(own, __builtin_ctzll(left));
-        uint64_t rows = __ballot(own == first) & left;
-        if (__popcll(rows) > kChunkTile) {
-            const int lane = threadIdx.x & 63;
-            rows = __ballot((rows >> lane & 1) && __popcll(rows & ((1ull << lane) - 1)) < kChunkTile);
-        }
-        left &= ~rows;
-        return rows;
     }
     // The next tile's adapter (-1: rows without one) and number of rows; false: there is none.
     __device__ __forceinline__ bool next(const LoraArgs& a, int* list_s, int& adapter, int& n) {
@@ -136,16 +132,18 @@ struct Tiles {
             n = __builtin_amdgcn_readfirstlane(tile.z);
             if (n == 0) return false;
             if (threadIdx.x < 64) list_s[lane] = a.order[tile.y + min(lane, n - 1)];
-            at += slots;
         } else {
-            if (!left) return false;
-            adapter = __builtin_amdgcn_readlane(own, __builtin_ctzll(left));
-            const uint64_t rows = take();
-            n = __popcll(rows);
-            if (threadIdx.x < 64 && (rows >> lane & 1))
-                list_s[__popcll(rows & ((1ull << lane) - 1))] = unit * kLoraChunk + lane;
-            for (int i = 1; i < slots && left; ++i) take();
+            const uint64_t before = (1ull << lane) - 1;
+            const uint64_t it = __ballot((starts >> lane & 1) && __popcll(starts & before) == at);
+            if (!it) return false;
+            const int src = __builtin_ctzll(it);
+            adapter = __builtin_amdgcn_readlane(own, src);
+            const uint32_t place = (uint32_t)(rank - __builtin_amdgcn_readlane(rank, src));
+            const bool mine = own == adapter && place < kChunkTile;
+            n = __popcll(__ballot(mine));
+            if (threadIdx.x < 64 && mine) list_s[place] = unit * kLoraChunk + lane;
         }
+        at += slots;
         __syncthreads();
         return true;
     }

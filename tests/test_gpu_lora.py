@@ -58,7 +58,7 @@ def reference(i, scale=True):
     R, L = A.shape[1], A.shape[0]
     who = i["adapter"].numpy()
     ref, err = Y.copy(), np.zeros_like(Y)
-    tiles, units = (T + 63) // 64, (K + 127) // 128
+    tiles, units = (T + 1) // 2 if T <= 256 else (T + 63) // 64, (K + 127) // 128
     each = -(-units // (4 * -(-(512 if R <= 32 else 256) // tiles)))
     splits = -(-units // (4 * each))
     chain = (each * 128 + 4 + splits) * U
