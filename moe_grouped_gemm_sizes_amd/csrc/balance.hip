@@ -15,25 +15,38 @@ namespace moegg {
 
 // ----------------------------------------------------------------- one token
 
-// A group of LPT lanes takes a token, VPL neighbouring experts a lane.
+// A group of LPT lanes takes a token, VPL neighbouring experts a lane.  Steps of 16
+// and 32 lanes swap rows of lanes in registers.
 template <int LPT>
 __device__ __forceinline__ float group_sum(float v) {
     v += __uint_as_float(lane_of<DPP_XOR1>(__float_as_uint(v)));
     v += __uint_as_float(lane_of<DPP_XOR2>(__float_as_uint(v)));
-    if (LPT >= 8) v += __uint_as_float(lane_of<DPP_HALF_MIRROR>(__float_as_uint(v)));
-    if (LPT >= 16) v += __uint_as_float(lane_of<DPP_MIRROR>(__float_as_uint(v)));
-    if (LPT >= 32) v += __shfl_xor(v, 16, 64);
-    if (LPT >= 64) v += __shfl_xor(v, 32, 64);
+    v += __uint_as_float(lane_of<DPP_HALF_MIRROR>(__float_as_uint(v)));
+    v += __uint_as_float(lane_of<DPP_MIRROR>(__float_as_uint(v)));
+    if (LPT >= 32) {
+        const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+    }
+    if (LPT >= 64) {
+        const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+    }
     return v;
 }
 template <int LPT>
 __device__ __forceinline__ float group_max(float v) {
     v = fmaxf(v, __uint_as_float(lane_of<DPP_XOR1>(__float_as_uint(v))));
     v = fmaxf(v, __uint_as_float(lane_of<DPP_XOR2>(__float_as_uint(v))));
-    if (LPT >= 8) v = fmaxf(v, __uint_as_float(lane_of<DPP_HALF_MIRROR>(__float_as_uint(v))));
-    if (LPT >= 16) v = fmaxf(v, __uint_as_float(lane_of<DPP_MIRROR>(__float_as_uint(v))));
-    if (LPT >= 32) v = fmaxf(v, __shfl_xor(v, 16, 64));
-    if (LPT >= 64) v = fmaxf(v, __shfl_xor(v, 32, 64));
+    v = fmaxf(v, __uint_as_float(lane_of<DPP_HALF_MIRROR>(__float_as_uint(v))));
+    v = fmaxf(v, __uint_as_float(lane_of<DPP_MIRROR>(__float_as_uint(v))));
+    if (LPT >= 32) {
+        const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+    }
+    if (LPT >= 64) {
+        const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+    }
     return v;
 }
 
@@ -62,13 +75,16 @@ __device__ __forceinline__ float probabilities(const float (&l)[VPL], bool sigmo
     return sigmoid || !(sum > 0.f) ? 0.f : top + logf(sum);
 }
 
-// The sequence that holds token t: the last one that starts at or before it (0 if none does).
+// The sequence that holds token t, the same for the whole wave: the last one that starts at or
+// before it (0 if none does).  64 offsets a step, one load up to 64 sequences.
 __device__ __forceinline__ int sequence_of(const int32_t* offsets, int S, int t) {
-    int lo = 0, hi = S;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (offsets[mid] <= t) lo = mid;
-        else hi = mid;
+    int lo = 0, n = S;
+    while (n > 1) {
+        const int step = (n + 63) / 64, i = ((int)threadIdx.x & 63) * step;
+        const uint64_t before = __ballot(i < n && offsets[lo + min(i, n - 1)] <= t);
+        const int last = max((int)__popcll(before) - 1, 0) * step;
+        lo += last;
+        n = min(step, n - last);
     }
     return lo;
 }
@@ -84,65 +100,22 @@ __device__ __forceinline__ void bounds_of(const int32_t* offsets, int s, int T, 
 
 // ----------------------------------------------------------------- forward
 
-// Sums over tokens [t0, t1) of one sequence, left in LDS.
-template <int WAVES, int VPL, int LPT>
-struct Piece {
-    static constexpr int kExperts = VPL * LPT, kTokens = 64 / LPT;
-    float p[WAVES][kExperts];
-    int n[kExperts];
-    float z[WAVES];
-
-    __device__ __forceinline__ void add(const BalanceArgs& a, int t0, int t1) {
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane % LPT;
-        for (int e = threadIdx.x; e < kExperts; e += WAVES * 64) n[e] = 0;
-        __syncthreads();
-        for (int64_t i = (int64_t)t0 * a.k + threadIdx.x; i < (int64_t)t1 * a.k; i += WAVES * 64) {
-            const int id = a.ids[i];
-            if (id >= 0 && id < a.E) atomicAdd(&n[id], 1);       // whole numbers: any order
-        }
-        float acc[VPL], zs = 0.f;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
-        for (int tw = t0 + wave * kTokens; tw < t1; tw += WAVES * kTokens) {
-            const int t = tw + lane / LPT;
-            const bool there = t < t1;
-            float l[VPL], v[VPL];
-            load_logits<VPL>(a.logits, min(t, t1 - 1), a.E, a.bf16, sub, l);
-            const float lse = probabilities<VPL, LPT>(l, a.sigmoid, v);
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) acc[i] += there ? v[i] : 0.f;
-            zs += there ? lse * lse : 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-#pragma unroll
-            for (int off = LPT; off < 64; off <<= 1) acc[i] += __shfl_xor(acc[i], off, 64);
-            if (lane < LPT) p[wave][sub * VPL + i] = acc[i];
-        }
-#pragma unroll
-        for (int off = LPT; off < 64; off <<= 1) zs += __shfl_xor(zs, off, 64);
-        if (lane == 0) z[wave] = zs;
-        __syncthreads();
-    }
-    __device__ __forceinline__ float sum_p(int e) const {
-        float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) s += p[w][e];
-        return s;
-    }
-    __device__ __forceinline__ float sum_z() const {
-        float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) s += z[w];
-        return s;
-    }
-};
-
 // Sum of 64-bit terms over the workgroup in a fixed order, in thread 0.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double v) {
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, false);
+    return v + __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
 __device__ __forceinline__ double block_sum_f64(double v, double* part_s) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-    if ((threadIdx.x & 63) == 0) part_s[threadIdx.x >> 6] = v;
+    v = dpp_add<DPP_SHR + 1, 0xF>(v);
+    v = dpp_add<DPP_SHR + 2, 0xF>(v);
+    v = dpp_add<DPP_SHR + 4, 0xF>(v);
+    v = dpp_add<DPP_SHR + 8, 0xF>(v);
+    v = dpp_add<DPP_BCAST15, 0xA>(v);
+    v = dpp_add<DPP_BCAST31, 0xC>(v);
+    if ((threadIdx.x & 63) == 63) part_s[threadIdx.x >> 6] = v;
     __syncthreads();
     double s = 0.;
     if (threadIdx.x == 0)
@@ -165,28 +138,131 @@ __device__ __forceinline__ void finish(const BalanceArgs& a, int s, int n, doubl
     }
 }
 
+// Bounds of sequences from one on, a lane each.
+struct Bounds {
+    int base, at;                        // first sequence held; this lane's offset
+
+    __device__ __forceinline__ void hold(const BalanceArgs& a, int s) {
+        base = s;
+        at = min(max(a.offsets[min(s + ((int)threadIdx.x & 63), a.S)], 0), a.T);
+    }
+    __device__ __forceinline__ void of(const BalanceArgs& a, int s, int& start, int& end) {
+        if (!a.offsets) {
+            start = 0;
+            end = a.T;
+            return;
+        }
+        if (s - base > 62) hold(a, s);
+        start = __builtin_amdgcn_readlane(at, s - base);
+        end = max(__builtin_amdgcn_readlane(at, s - base + 1), start);
+    }
+};
+
 // Sums of a tile of tokens, one row of them for each sequence that it meets.
 // Tiles and sequences both go up along the tokens, so tile + sequence tells these
-// rows apart.
+// rows apart.  32 tokens at a time, whose logits and assignments are on their way
+// while their sequences are looked up; a sequence's sums are in registers until it
+// ends.  8191 tokens over 256 experts in 16 sequences: ...
+constexpr int kTileStep = 32;
 template <int VPL, int LPT>
-__global__ __launch_bounds__(256) void balance_tile_kernel(BalanceArgs a) {
-    __shared__ Piece<4, VPL, LPT> piece;
+constexpr int kTileWaves = VPL == 16 || LPT == 16 ? 8 : 16;  // LDS for 1024 experts; 4 tokens a wave up to 64
+
+template <int VPL, int LPT>
+__global__ __launch_bounds__((kTileWaves<VPL, LPT> * 64)) void balance_tile_kernel(BalanceArgs a) {
+    constexpr int kWaves = kTileWaves<VPL, LPT>, kThreads = kWaves * 64, kExperts = VPL * LPT, kTokens = 64 / LPT;
+    constexpr int kTurns = kTileStep / (kWaves * kTokens), kIds = kTileStep * kRouteMaxTopK / kThreads;
+    __shared__ float p_s[kWaves][kExperts], z_s[kWaves];
+    __shared__ int n_s[kExperts];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane % LPT, token = wave * kTokens + lane / LPT;
     const int t0 = (int)blockIdx.x * a.tile_tokens, t1 = min(t0 + a.tile_tokens, a.T);
-    for (int s = a.offsets ? sequence_of(a.offsets, a.S, t0) : 0; s < a.S; ++s) {
-        int start, end;
-        bounds_of(a.offsets, s, a.T, start, end);
-        if (start >= t1) break;
-        start = max(start, t0);
-        end = min(end, t1);
-        if (start >= end) continue;
-        piece.add(a, start, end);
-        const int64_t row = (int64_t)blockIdx.x + s;
-        for (int e = threadIdx.x; e < a.E; e += 256) {
-            a.part_p[row * a.E + e] = piece.sum_p(e);
-            a.part_n[row * a.E + e] = piece.n[e];
+    float acc[VPL], zs = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
+    Bounds bounds{};
+    int s = 0, start = 0, end = 0;
+    for (int t = t0; t < t1; t += kTileStep) {
+        const int last = min(t + kTileStep, t1);
+        float p[kTurns][VPL], z[kTurns];
+        int id[kIds], of[kIds];                              // an assignment and its token
+#pragma unroll
+        for (int r = 0; r < kTurns; ++r)
+            load_logits<VPL>(a.logits, min(t + token + r * kWaves * kTokens, last - 1), a.E, a.bf16, sub, p[r]);
+#pragma unroll
+        for (int i = 0; i < kIds; ++i) {
+            const int j = i * kThreads + (int)threadIdx.x;
+            id[i] = j < (last - t) * a.k ? a.ids[(int64_t)t * a.k + j] : -1;
+            if (id[i] >= a.E) id[i] = -1;
+            of[i] = t + j / a.k;
         }
-        if (threadIdx.x == 0) a.part_z[row] = piece.sum_z();
-        __syncthreads();
+        if (t == t0) {
+            if (a.offsets) {
+                s = sequence_of(a.offsets, a.S, t0);
+                bounds.hold(a, s);
+            }
+            bounds.of(a, s, start, end);
+            for (int e = threadIdx.x; e < kExperts; e += kThreads) n_s[e] = 0;
+            lds_barrier();
+        }
+#pragma unroll
+        for (int r = 0; r < kTurns; ++r) {
+            const float lse = probabilities<VPL, LPT>(p[r], a.sigmoid, p[r]);
+            z[r] = lse * lse;
+        }
+        for (;;) {                                           // the sequences that these tokens are of
+            const int from = max(start, t), to = min(end, last);
+#pragma unroll
+            for (int r = 0; r < kTurns; ++r) {
+                const int at = t + token + r * kWaves * kTokens;
+                const bool in = at >= from && at < to;
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) acc[i] += in ? p[r][i] : 0.f;
+                zs += in ? z[r] : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < kIds; ++i)
+                if (id[i] >= 0 && of[i] >= from && of[i] < to) atomicAdd(&n_s[id[i]], 1);   // whole numbers: any order
+            if (end > last && last < t1) break;              // the sequence goes on in the tile's next step
+            // the sequence's sums in this tile, if it has any tokens there
+            if (max(start, t0) < min(end, t1)) {
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) {
+#pragma unroll
+                    for (int off = LPT; off < 64; off <<= 1) acc[i] += __shfl_xor(acc[i], off, 64);
+                    if (lane < LPT) p_s[wave][sub * VPL + i] = acc[i];
+                    acc[i] = 0.f;
+                }
+#pragma unroll
+                for (int off = LPT; off < 64; off <<= 1) zs += __shfl_xor(zs, off, 64);
+                if (lane == 0) z_s[wave] = zs;
+                zs = 0.f;
+                lds_barrier();
+                const int64_t row = (int64_t)blockIdx.x + s;
+                for (int e = threadIdx.x; e < kExperts; e += kThreads) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kWaves; ++w) sum += p_s[w][e];
+                    if (e < a.E) {
+                        a.part_p[row * a.E + e] = sum;
+                        a.part_n[row * a.E + e] = n_s[e];
+                    }
+                    n_s[e] = 0;
+                }
+                if (threadIdx.x == 0) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kWaves; ++w) sum += z_s[w];
+                    a.part_z[row] = sum;
+                }
+                lds_barrier();
+            }
+            if (end > last) break;                           // or in the next tile
+            if (s + 1 >= a.S) {
+                start = end = a.T;                           // tokens past the last sequence
+                break;
+            }
+            bounds.of(a, ++s, start, end);
+            if (start >= last) break;
+        }
     }
 }
 
@@ -206,9 +282,20 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a) {
     if (start < end) {
         const int first = start / a.tile_tokens, last = (end - 1) / a.tile_tokens;
         if (e < a.E)
-            for (int c = first + part; c <= last; c += parts) {
-                p += a.part_p[((int64_t)c + s) * a.E + e];
-                n += a.part_n[((int64_t)c + s) * a.E + e];
+            for (int c = first + part; c <= last; c += 4 * parts) {
+                float v[4];
+                int m[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {                    // four rows on their way together
+                    const int64_t at = ((int64_t)min(c + i * parts, last) + s) * a.E + e;
+                    v[i] = a.part_p[at];
+                    m[i] = a.part_n[at];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    p += c + i * parts <= last ? v[i] : 0.f;
+                    n += c + i * parts <= last ? m[i] : 0;
+                }
             }
         if (a.z_loss)
             for (int c = first + (int)threadIdx.x; c <= last; c += 1024) z += a.part_z[(int64_t)c + s];
@@ -233,13 +320,27 @@ template <int VPL, int LPT>
 __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceBackwardArgs a) {
     constexpr int kTokens = 64 / LPT;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane % LPT;
-    const int64_t t = ((int64_t)blockIdx.x * 4 + wave) * kTokens + lane / LPT;
+    const int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * kTokens, t = t0 + lane / LPT;
+    if (t0 >= a.T) return;
     const int64_t row = t < a.T ? t : a.T - 1;
-    float l[VPL], p[VPL], o[VPL];
+    float l[VPL], p[VPL], o[VPL], before[VPL];
     load_logits<VPL>(a.logits, row, a.E, a.bf16, sub, l);
-    const int s = a.offsets ? sequence_of(a.offsets, a.S, (int)row) : 0;
-    int start, end;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) before[i] = 0.f;
+    if (a.before) {
+        if (a.bf16) {
+            uint16_t b[VPL];
+            load_row<uint16_t, VPL>((const uint16_t*)a.before + row * a.E, a.E, sub, b);
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) before[i] = __uint_as_float((uint32_t)b[i] << 16);
+        } else {
+            load_row<float, VPL>((const float*)a.before + row * a.E, a.E, sub, before);
+        }
+    }
+    // the wave's first token's sequence, and from there on to this one's
+    int s = a.offsets ? sequence_of(a.offsets, a.S, (int)t0) : 0, start, end;
     bounds_of(a.offsets, s, a.T, start, end);
+    while (row >= end && s + 1 < a.S) bounds_of(a.offsets, ++s, a.T, start, end);
     const bool in = row >= start && row < end;
     const float n = (float)max(end - start, 1);
     const float c = in ? a.d_loss[s] * ((float)a.E / (float)a.k) / n / n : 0.f;
@@ -261,24 +362,14 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceBackwardAr
         else o[i] = __builtin_fmaf(p[i], dz * lse, o[i]);
     }
     if (t >= a.T) return;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) o[i] += before[i];
     if (a.bf16) {
         __bf16 r[VPL];
-        if (a.before) {
-            uint16_t b[VPL];
-            load_row<uint16_t, VPL>((const uint16_t*)a.before + t * a.E, a.E, sub, b);
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) o[i] += __uint_as_float((uint32_t)b[i] << 16);
-        }
 #pragma unroll
         for (int i = 0; i < VPL; ++i) r[i] = (__bf16)o[i];
         store_row<__bf16, VPL>((__bf16*)a.d_logits + t * a.E, a.E, sub, r);
     } else {
-        if (a.before) {
-            float b[VPL];
-            load_row<float, VPL>((const float*)a.before + t * a.E, a.E, sub, b);
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) o[i] += b[i];
-        }
         store_row<float, VPL>((float*)a.d_logits + t * a.E, a.E, sub, o);
     }
 }
@@ -288,7 +379,7 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceBackwardAr
 template <int VPL, int LPT>
 static hipError_t balance_as(const BalanceArgs& a, hipStream_t s) {
     if (a.T > 0) {
-        balance_tile_kernel<VPL, LPT><<<(a.T + a.tile_tokens - 1) / a.tile_tokens, 256, 0, s>>>(a);
+        balance_tile_kernel<VPL, LPT><<<(a.T + a.tile_tokens - 1) / a.tile_tokens, kTileWaves<VPL, LPT> * 64, 0, s>>>(a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
