@@ -162,7 +162,9 @@ struct Bounds {
 // Tiles and sequences both go up along the tokens, so tile + sequence tells these
 // rows apart.  32 tokens at a time, whose logits and assignments are on their way
 // while their sequences are looked up; a sequence's sums are in registers until it
-// ends.  8191 tokens over 256 experts in 16 sequences: ...
+// ends.  8191 tokens over 256 experts in 16 sequences: 7 us, of which a launch is 1.75 and
+// three loads one after the other most of the rest (11 us with the sequences looked up first, in 4
+// waves of 8 tokens).
 constexpr int kTileStep = 32;
 template <int VPL, int LPT>
 constexpr int kTileWaves = VPL == 16 || LPT == 16 ? 8 : 16;  // LDS for 1024 experts; 4 tokens a wave up to 64
