@@ -85,9 +85,10 @@ class MoELayer:
         mg.combine(Y, r["row_of"], out, r["weights"])
         return out, dict(r, x=x, A=A, A_scale=A_scale, ckpt=ckpt, ckpt_scale=ckpt_scale, Y=Y)
 
-    def backward(self, dout, kept):
+    def backward(self, dout, kept, d_logits_of=None):
         """Gradients of x (bf16), the router (a bf16 product, as fp32) and the expert weights: W1 fp32 [E, hidden,
-        2 inter] and W2 [E, inter, hidden], as the K-grouped product writes them."""
+        2 inter] and W2 [E, inter, hidden], as the K-grouped product writes them.  d_logits_of: adds what else the logits
+        get (of a balance loss) to their gradient, in place."""
         T, rows, I, K, E = dout.shape[0], dout.shape[0] * self.k, self.inter, self.hidden, self.E
         m, row_of = kept["m_sizes"], kept["row_of"]
         dY, dY_scale = self._fp8(rows, K)
@@ -118,6 +119,8 @@ class MoELayer:
         mg.grouped_gemm_k_grouped(H_k, dY_k, dW2, m, self.ws, H_ks, dY_ks)
         d_logits = self._new(T, E, dtype=kept["logits"].dtype)
         mg.route_backward(kept["logits"], kept["ids"], d_weights, d_logits, scale=self.scale)
+        if d_logits_of is not None:
+            d_logits_of(d_logits)
         dx += d_logits @ self.router
         return dict(x=dx, router=(d_logits.t() @ kept["x"]).float(), W1=dW1, W2=dW2)
 
