@@ -6,7 +6,8 @@
 // find these by themselves: a wave looks at 64 consecutive rows, a lane each, and
 // takes the adapters among them one by one, up to 16 rows a tile.  Beyond, a first
 // launch sorts windows of 8192 rows by their adapters, so that an adapter's weights
-// are read for 64 rows together whatever the order of the rows.
+// are read for 64 rows together whatever the order of the rows (chunks too with more
+// adapters than LDS counts).
 #include <hip/hip_runtime.h>
 
 #include "block.hpp"
@@ -16,11 +17,7 @@
 
 namespace moegg {
 
-#ifndef ET
-#define ET 256
-#endif
-constexpr int kThreads = 256;             // of the first product
-constexpr int kExpandThreads = ET;       // of the second: as many columns of out
+constexpr int kThreads = 256;             // and columns of out that a workgroup of the second product takes
 constexpr int kTile = kLoraChunk;         // rows of a tile
 constexpr int kChunkTile = 16;            // and of one that was not sorted
 
@@ -31,7 +28,7 @@ constexpr int kChunkTile = 16;            // and of one that was not sorted
 // does not depend on its place.
 __global__ __launch_bounds__(1024) void lora_sort_kernel(LoraArgs a, int copy) {
     extern __shared__ int count_s[];                         // [L + 1]: rows of each adapter, then their first place
-    __shared__ int rows_s[16], tiles_s[16];
+    __shared__ int rows_s[16], tiles_s[16], all_tiles_s;
     constexpr int kEach = kLoraWindow / 1024;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, first = (int)blockIdx.x * kLoraWindow;
     int4* tiles = a.tiles + (int64_t)blockIdx.x * a.max_tiles;
@@ -79,9 +76,10 @@ __global__ __launch_bounds__(1024) void lora_sort_kernel(LoraArgs a, int copy) {
     }
     __syncthreads();
     int place = rows_end - rows, tile = n_end - n;
-    for (int w = 0; w < wave; ++w) {
-        place += rows_s[w];
-        tile += tiles_s[w];
+#pragma unroll
+    for (int w = 0; w < 15; ++w) {
+        place += w < wave ? rows_s[w] : 0;
+        tile += w < wave ? tiles_s[w] : 0;
     }
     for (int k = k0; k < k1; ++k) {
         const int c = count_s[k];
@@ -90,9 +88,9 @@ __global__ __launch_bounds__(1024) void lora_sort_kernel(LoraArgs a, int copy) {
             for (int b = 0; b < c; b += kTile) tiles[tile++] = int4{k < a.L ? k : -1, first + place + b, min(kTile, c - b), 0};
         place += c;
     }
-    if (threadIdx.x == 1023) tiles_s[0] = tile;
+    if (threadIdx.x == 1023) all_tiles_s = tile;             // a word of its own: tiles_s is still being read
     __syncthreads();
-    for (int i = tiles_s[0] + (int)threadIdx.x; i < a.max_tiles; i += 1024) tiles[i] = int4{-1, 0, 0, 0};
+    for (int i = all_tiles_s + (int)threadIdx.x; i < a.max_tiles; i += 1024) tiles[i] = int4{-1, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
         if (key[i] >= 0) a.order[first + count_s[key[i]] + rank[i]] = first + i * 1024 + (int)threadIdx.x;
@@ -153,7 +151,9 @@ struct Tiles {
 
 // A workgroup takes a tile and a part of K, its waves a share of that each; their
 // sums meet in LDS.  D = X A^T in blocks of 16 rows x 16 ranks.  K goes in units of 128
-// columns, whole lines, all of whose loads are in flight together.
+// columns, whole lines, all of whose loads are in flight together.  4096 rows of 7168 to a rank of
+// 16: 15 us for 59 MB; 8 waves a workgroup (22 us: one of them a CU) and loads of half a unit
+// ahead of the products (15 us) do not pay.
 constexpr int kUnit = 128;
 
 template <int RT, int CT>
@@ -264,19 +264,24 @@ __device__ __forceinline__ void swap_halves(u32x4& first, u32x4& second) {
     if (odd) first = got;
     else second = got;
 }
-// Y and B are on their way while U's parts are added.
+
+// Y and B are on their way while U's parts are added.  4096 rows, rank 16, 4096 columns: 17 us for 67 MB
+// of Y and out; 8191 rows, rank 64, 7168 columns: 60 us for 235 MB, 8 of which B's fragments
+// and 14 U's parts cost beside them (both without any stores 10).  Accesses in halves of lines
+// cost 2 us of the first, two panels of columns a workgroup or 512 threads nothing of either; fewer
+// registers (128) a third of the second.
 template <int RT, int RS>
 __device__ __forceinline__ void expand(const LoraArgs& a, const int* list_s, uint16_t (*u_s)[RS * 64 + 8], int n,
                                        int adapter, int col) {
     const int lane = threadIdx.x & 63, l16 = lane & 15, grp = lane >> 4;
     // U: four ranks a thread at a time, summed over the parts of K in order.  Loads return in the
     // order in which they were sent: the last of U's go before those of Y and B.
-    constexpr int kItems = RT * 16 * RS * 8, kEach = (kItems + kExpandThreads - 1) / kExpandThreads;
+    constexpr int kItems = RT * 16 * RS * 8, kEach = (kItems + kThreads - 1) / kThreads;
     constexpr int kParts = RT == 1 ? 8 : (RT == 2 ? 4 : 2);      // loaded together
     v4f u[kEach], p[kParts][kEach];
     const int64_t step = (int64_t)a.T * a.R;
     auto part = [&](int j, int s) {
-        const int i = j * kExpandThreads + (int)threadIdx.x, row = i / (RS * 8), rank = i % (RS * 8) * 4;
+        const int i = j * kThreads + (int)threadIdx.x, row = i / (RS * 8), rank = i % (RS * 8) * 4;
         return row < n && rank < a.R && s < a.splits ? *(const v4f*)(a.U + s * step + (int64_t)list_s[row] * a.R + rank)
                                                     : v4f{0, 0, 0, 0};
     };
@@ -323,7 +328,7 @@ __device__ __forceinline__ void expand(const LoraArgs& a, const int* list_s, uin
     add();
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
-        const int i = j * kExpandThreads + (int)threadIdx.x, row = i / (RS * 8), rank = i % (RS * 8) * 4;
+        const int i = j * kThreads + (int)threadIdx.x, row = i / (RS * 8), rank = i % (RS * 8) * 4;
         if (i >= kItems) break;
         uint16_t hi[4], lo[4];
 #pragma unroll
@@ -362,11 +367,8 @@ __device__ __forceinline__ void expand(const LoraArgs& a, const int* list_s, uin
     }
 }
 
-#ifndef EB
-#define EB 2
-#endif
 template <int RS, bool SORTED>
-__global__ __launch_bounds__(kExpandThreads, EB) void lora_expand_kernel(LoraArgs a, int slots, int panels) {
+__global__ __launch_bounds__(kThreads, 2) void lora_expand_kernel(LoraArgs a, int slots, int panels) {
     __shared__ int list_s[kTile];
     __shared__ __align__(16) uint16_t u_s[kTile][RS * 64 + 8];   // 16 bytes more: 16 rows' pieces on all banks
     const int panel = blockIdx.x % panels, slot = blockIdx.x / panels % slots, unit = blockIdx.x / panels / slots;
@@ -375,17 +377,17 @@ __global__ __launch_bounds__(kExpandThreads, EB) void lora_expand_kernel(LoraArg
     int adapter, n;
     while (tiles.next(a, list_s, adapter, n)) {
         if (adapter < 0) {                                   // copied: 8 columns a thread, 8 rows together
-            const int c = panel * kExpandThreads + (int)threadIdx.x % (kExpandThreads / 8) * 8;
-            for (int i = (int)threadIdx.x / (kExpandThreads / 8); i < n; i += 8) {
+            const int c = panel * kThreads + (int)threadIdx.x % (kThreads / 8) * 8;
+            for (int i = (int)threadIdx.x / (kThreads / 8); i < n; i += 8) {
                 const int64_t at = (int64_t)list_s[i] * a.N + c;
                 if (c < a.N) *(u32x4*)((uint16_t*)a.out + at) = *(const u32x4*)((const uint16_t*)a.Y + at);
             }
         } else if (!SORTED || n <= 16) {
-            expand<1, RS>(a, list_s, u_s, n, adapter, panel * kExpandThreads + wave * 64);
+            expand<1, RS>(a, list_s, u_s, n, adapter, panel * kThreads + wave * 64);
         } else if (n <= 32) {
-            expand<2, RS>(a, list_s, u_s, n, adapter, panel * kExpandThreads + wave * 64);
+            expand<2, RS>(a, list_s, u_s, n, adapter, panel * kThreads + wave * 64);
         } else {
-            expand<4, RS>(a, list_s, u_s, n, adapter, panel * kExpandThreads + wave * 64);
+            expand<4, RS>(a, list_s, u_s, n, adapter, panel * kThreads + wave * 64);
         }
         __syncthreads();
     }
@@ -403,13 +405,13 @@ static int lora_slots(int most, int64_t others, int goal) {
 template <int CT, int RS, bool SORTED>
 static hipError_t lora_as(const LoraArgs& a, hipStream_t s) {
     const int64_t units = SORTED ? (a.T + kLoraWindow - 1) / kLoraWindow : (a.T + kLoraChunk - 1) / kLoraChunk;
-    const int panels = (a.N + kExpandThreads - 1) / kExpandThreads;
+    const int panels = (a.N + kThreads - 1) / kThreads;
     int slots = lora_slots(a.max_tiles, units * a.splits, 2048);
     lora_shrink_kernel<CT, SORTED><<<(unsigned)(units * slots * a.splits), kThreads, 0, s>>>(a, slots);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     slots = lora_slots(a.max_tiles, units * panels, 4096);
-    lora_expand_kernel<RS, SORTED><<<(unsigned)(units * slots * panels), kExpandThreads, 0, s>>>(a, slots, panels);
+    lora_expand_kernel<RS, SORTED><<<(unsigned)(units * slots * panels), kThreads, 0, s>>>(a, slots, panels);
     return hipGetLastError();
 }
 
