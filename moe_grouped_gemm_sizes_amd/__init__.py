@@ -149,7 +149,8 @@ EXPORTS = {
     "moegg_rms_norm_workspace_bytes": (_SZ, [_I32, _I32]),
     "moegg_rms_norm_backward": (_I32, [_VP, _VP, _VP, _I32, _VP, _VP, _VP, _VP, _I32, _I32, _VP, _SZ, _VP]),
     "moegg_balance_loss_workspace_bytes": (_SZ, [_I32, _I32, _I32]),
-    "moegg_balance_loss": (_I32, [_VP, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _I32, _I32, _I32, _I32, _VP, _SZ, _VP]),
+    "moegg_balance_loss": (_I32, [_VP, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _I32, _I32, _I32, _I32, _VP, _SZ,
+                                  _VP]),
     "moegg_balance_loss_backward": (_I32, [_VP, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _I32, _I32, _I32, _I32, _VP]),
     "moegg_lora_workspace_bytes": (_SZ, [_I32, _I32, _I32]),
     "moegg_lora": (_I32, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _I32, _I32, _I32, _I32, _VP, _SZ, _VP]),
@@ -855,6 +856,14 @@ def _ws_spec(ws, need: int, what: str):
     return n, (ws, "ws", (n,), torch.uint8)
 
 
+def _stream_for(t, stream):
+    """The stream of a call on t's device, which has to be the current one unless a stream is given: launches go
+    to the current device."""
+    if stream is None and t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"tensors on cuda:{t.get_device()}, the current device is cuda:{torch.cuda.current_device()}")
+    return _stream(stream)
+
+
 def _optional(t, name: str, shape, kind):
     return (t, name, shape, kind) if t is not None else _ABSENT
 
@@ -894,7 +903,7 @@ def rms_norm(x, weight, *, y=None, q=None, q_scale=None, residual=None, sum_out=
         (x, "x", (T, K), _H), _optional(residual, "residual", (T, K), _H), weight_spec,
         _optional(sum_out, "sum_out", (T, K), _H), _optional(y, "y", (T, K), _H), q_spec, scale_spec,
         _optional(rstd, "rstd", (T,), _F))
-    _check(lib().moegg_rms_norm(px, pr, pw, weight_kind, eps, ps, py, pq, pqs, pd, T, K, code, _stream(stream)),
+    _check(lib().moegg_rms_norm(px, pr, pw, weight_kind, eps, ps, py, pq, pqs, pd, T, K, code, _stream_for(x, stream)),
            "moegg_rms_norm")
 
 
@@ -909,8 +918,8 @@ def rms_norm_workspace(T: int, K: int, device="cuda") -> torch.Tensor:
 
 def rms_norm_backward(dy, h, weight, rstd, dx, d_weight=None, ws=None, *, d_sum=None, stream=None):
     """dx bf16 [T, K], the gradient of x and of the residual, and d_weight fp32 [K] (None: left out) from dy bf16 [T, K]
-    (see moegg.h); h is rms_norm's sum_out (or x), rstd as it wrote it, d_sum bf16 [T, K] the gradient that arrives at the
-    sum itself.  ws: rms_norm_workspace(T, K), or of more tokens; needed for d_weight.  dx may be dy, h or d_sum."""
+    (see moegg.h); h is rms_norm's sum_out (or x), rstd as it wrote it, d_sum bf16 [T, K] the gradient that arrives at
+    the sum itself.  ws: rms_norm_workspace(T, K), or of more tokens; needed for d_weight.  dx may be dy, h or d_sum."""
     T, K = _matrix(dy, "dy", (_H,))
     weight_kind, weight_spec = _norm_weight(weight, K)
     n, ws_spec = 0, _ABSENT
@@ -918,9 +927,10 @@ def rms_norm_backward(dy, h, weight, rstd, dx, d_weight=None, ws=None, *, d_sum=
         n, ws_spec = _ws_spec(ws, rms_norm_workspace_bytes(T, K), f"rms_norm_workspace_bytes({T}, {K})")
     pd, ph, pw, pr, ps, px, pdw, pws = _pointers(
         (dy, "dy", (T, K), _H), (h, "h", (T, K), _H), weight_spec, (rstd, "rstd", (T,), _F),
-        _optional(d_sum, "d_sum", (T, K), _H), (dx, "dx", (T, K), _H), _optional(d_weight, "d_weight", (K,), _F), ws_spec)
-    _check(lib().moegg_rms_norm_backward(pd, ph, pw, weight_kind, pr, ps, px, pdw, T, K, pws, n, _stream(stream)),
-           "moegg_rms_norm_backward")
+        _optional(d_sum, "d_sum", (T, K), _H), (dx, "dx", (T, K), _H), _optional(d_weight, "d_weight", (K,), _F),
+        ws_spec)
+    _check(lib().moegg_rms_norm_backward(pd, ph, pw, weight_kind, pr, ps, px, pdw, T, K, pws, n,
+                                         _stream_for(dy, stream)), "moegg_rms_norm_backward")
 
 
 @functools.lru_cache(maxsize=4096)
@@ -949,7 +959,7 @@ def balance_loss(logits, ids, loss, counts, ws, *, probs=None, z_loss=None, seq_
         (loss, "loss", (S,), _F), _optional(z_loss, "z_loss", (S,), _F), (counts, "counts", (S, E), _I),
         _optional(probs, "probs", (S, E), _F), ws_spec)
     _check(lib().moegg_balance_loss(l, LOGITS_BF16 if kind is _H else LOGITS_FP32, i, o, pl, pz, pc, pp, T, E, k, S,
-                                    score, pw, n, _stream(stream)), "moegg_balance_loss")
+                                    score, pw, n, _stream_for(logits, stream)), "moegg_balance_loss")
 
 
 def balance_loss_backward(logits, counts, d_loss, d_logits, *, k: int, d_z_loss=None, seq_offsets=None,
@@ -966,8 +976,8 @@ def balance_loss_backward(logits, counts, d_loss, d_logits, *, k: int, d_z_loss=
         _optional(seq_offsets, "seq_offsets", (S + 1,), _I), (d_loss, "d_loss", (S,), _F),
         _optional(d_z_loss, "d_z_loss", (S,), _F), _optional(before, "before", (T, E), kind),
         (d_logits, "d_logits", (T, E), kind))
-    _check(lib().moegg_balance_loss_backward(l, LOGITS_BF16 if kind is _H else LOGITS_FP32, c, o, dl, dz, b, d, T, E, k, S,
-                                             score, _stream(stream)), "moegg_balance_loss_backward")
+    _check(lib().moegg_balance_loss_backward(l, LOGITS_BF16 if kind is _H else LOGITS_FP32, c, o, dl, dz, b, d, T, E, k,
+                                             S, score, _stream_for(logits, stream)), "moegg_balance_loss_backward")
 
 
 @functools.lru_cache(maxsize=4096)
@@ -980,8 +990,8 @@ def lora_workspace(T: int, K: int, R: int, device="cuda") -> torch.Tensor:
 
 
 def lora(X, A, B, adapter, Y, out, ws, *, scale=None, stream=None):
-    """out[t] = Y[t] + scale[a] * (X[t] A_a^T) B_a^T with a = adapter[t], or Y[t] where that is no adapter (see moegg.h).
-    X bf16 [T, K], Y and out bf16 [T, N] (out may be Y), A bf16 [L, R, K], B bf16 [L, N, R], adapter int32 [T], scale
+    """out[t] = Y[t] + scale[a] * (X[t] A_a^T) B_a^T with a = adapter[t], or Y[t] where that is no adapter (see
+    moegg.h).  X bf16 [T, K], Y and out bf16 [T, N] (out may be Y), A bf16 [L, R, K], B bf16 [L, N, R], adapter int32 [T], scale
     fp32 [L].  ws: lora_workspace(T, K, R), or of more rows."""
     T, K = _matrix(X, "X", (_H,))
     N = _matrix(Y, "Y", (_H,))[1]
@@ -992,7 +1002,7 @@ def lora(X, A, B, adapter, Y, out, ws, *, scale=None, stream=None):
     px, pa, pb, ps, pi, py, po, pw = _pointers(
         (X, "X", (T, K), _H), (A, "A", (L, R, K), _H), (B, "B", (L, N, R), _H), _optional(scale, "scale", (L,), _F),
         (adapter, "adapter", (T,), _I), (Y, "Y", (T, N), _H), (out, "out", (T, N), _H), ws_spec)
-    _check(lib().moegg_lora(px, pa, pb, ps, pi, py, po, T, K, N, R, L, pw, n, _stream(stream)), "moegg_lora")
+    _check(lib().moegg_lora(px, pa, pb, ps, pi, py, po, T, K, N, R, L, pw, n, _stream_for(X, stream)), "moegg_lora")
 
 
 def stats_read(ws: torch.Tensor, stream=None) -> Stats:
