@@ -883,7 +883,7 @@ size_t moegg_lora_workspace_bytes(int T, int K, int R);
  *            not touched.
  * The inner product is summed in fp32 and enters the outer one as two bf16 (to
  * 2^-16 of it); scale and Y come in fp32, with one rounding at the end.  Only
- * adapters that some row has are read.  Two launches up to 256 rows or from 16384
+ * adapters that some row has are read.  Two launches up to 128 rows or from 16384
  * adapters on, else three.
  * K, N and R are multiples of 8, R = 8..128, T up to 2^24 and T / 64 * N / 256 up to
  * 2^23: UNSUPPORTED otherwise.  X, A, B, Y and out 16-byte aligned, scale and adapter 4.

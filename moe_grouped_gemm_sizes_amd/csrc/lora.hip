@@ -2,7 +2,7 @@
 //     out[t] = Y[t] + scale_a (X[t] A_a^T) B_a^T,   a the adapter of row t.
 //
 // Two products with a rank of 8 to 128, so that rows and weights are moved and little
-// is computed.  Both take tiles of rows with one adapter.  Up to 256 rows the kernels
+// is computed.  Both take tiles of rows with one adapter.  Up to 128 rows the kernels
 // find these by themselves: a wave looks at 64 consecutive rows, a lane each, and
 // takes the adapters among them one by one, up to 16 rows a tile.  Beyond, a first
 // launch sorts windows of 8192 rows by their adapters, so that an adapter's weights
@@ -28,7 +28,8 @@ constexpr int kChunkTile = 16;            // and of one that was not sorted
 // does not depend on its place.
 __global__ __launch_bounds__(1024) void lora_sort_kernel(LoraArgs a, int copy) {
     extern __shared__ int count_s[];                         // [L + 1]: rows of each adapter, then their first place
-    __shared__ int rows_s[16], tiles_s[16], all_tiles_s;
+    __shared__ uint32_t both_s[16];
+    __shared__ int all_tiles_s;
     constexpr int kEach = kLoraWindow / 1024;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, first = (int)blockIdx.x * kLoraWindow;
     int4* tiles = a.tiles + (int64_t)blockIdx.x * a.max_tiles;
@@ -54,33 +55,27 @@ __global__ __launch_bounds__(1024) void lora_sort_kernel(LoraArgs a, int copy) {
         }
     }
     __syncthreads();
-    // places and tiles before each adapter: a run of adapters a thread
+    // places and tiles before each adapter: a run of adapters a thread, rows and tiles as the
+    // halves of a word (8192 and 8320 at most)
     const int per = (a.L + 1024) / 1024, k0 = min((int)threadIdx.x * per, a.L + 1), k1 = min(k0 + per, a.L + 1);
-    int rows = 0, n = 0;
+    uint32_t both = 0;
     for (int k = k0; k < k1; ++k) {
-        rows += count_s[k];
-        if (k < a.L || copy) n += (count_s[k] + kTile - 1) / kTile;
+        const uint32_t c = count_s[k], n = k < a.L || copy ? (c + kTile - 1) / kTile : 0;
+        both += n << 16 | c;
     }
-    int rows_end = rows, n_end = n;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int r = __shfl_up(rows_end, d, 64), m = __shfl_up(n_end, d, 64);
-        if (lane >= d) {
-            rows_end += r;
-            n_end += m;
-        }
-    }
-    if (lane == 63) {
-        rows_s[wave] = rows_end;
-        tiles_s[wave] = n_end;
-    }
+    uint32_t end = both;
+    end += dpp<DPP_SHR + 1>(0, end);
+    end += dpp<DPP_SHR + 2>(0, end);
+    end += dpp<DPP_SHR + 4>(0, end);
+    end += dpp<DPP_SHR + 8>(0, end);
+    end += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)end, DPP_BCAST15, 0xA, 0xF, false);
+    end += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)end, DPP_BCAST31, 0xC, 0xF, false);
+    if (lane == 63) both_s[wave] = end;
     __syncthreads();
-    int place = rows_end - rows, tile = n_end - n;
+    end -= both;
 #pragma unroll
-    for (int w = 0; w < 15; ++w) {
-        place += w < wave ? rows_s[w] : 0;
-        tile += w < wave ? tiles_s[w] : 0;
-    }
+    for (int w = 0; w < 15; ++w) end += w < wave ? both_s[w] : 0u;
+    int place = (int)(end & 0xFFFFu), tile = (int)(end >> 16);
     for (int k = k0; k < k1; ++k) {
         const int c = count_s[k];
         count_s[k] = place;
@@ -88,7 +83,7 @@ __global__ __launch_bounds__(1024) void lora_sort_kernel(LoraArgs a, int copy) {
             for (int b = 0; b < c; b += kTile) tiles[tile++] = int4{k < a.L ? k : -1, first + place + b, min(kTile, c - b), 0};
         place += c;
     }
-    if (threadIdx.x == 1023) all_tiles_s = tile;             // a word of its own: tiles_s is still being read
+    if (threadIdx.x == 1023) all_tiles_s = tile;             // a word of its own: both_s is still being read
     __syncthreads();
     for (int i = all_tiles_s + (int)threadIdx.x; i < a.max_tiles; i += 1024) tiles[i] = int4{-1, 0, 0, 0};
 #pragma unroll

@@ -58,7 +58,7 @@ def reference(i, scale=True):
     R, L = A.shape[1], A.shape[0]
     who = i["adapter"].numpy()
     ref, err = Y.copy(), np.zeros_like(Y)
-    tiles, units = (T + 1) // 2 if T <= 256 else (T + 63) // 64, (K + 127) // 128
+    tiles, units = (T + 1) // 2 if T <= 128 else (T + 63) // 64, (K + 127) // 128
     each = -(-units // (4 * -(-(512 if R <= 32 else 256) // tiles)))
     splits = -(-units // (4 * each))
     chain = (each * 128 + 4 + splits) * U
@@ -96,7 +96,8 @@ def test_rows_in_any_order(T, K, N, R, L):
     check(i, scale=False, in_place=True)
 
 
-@pytest.mark.parametrize("T,K,N,R,L", [(256, 64, 64, 8, 7), (257, 64, 72, 16, 300), (1000, 128, 264, 32, 1), (4096, 72, 40, 64, 64),
+@pytest.mark.parametrize("T,K,N,R,L", [(128, 2048, 64, 8, 9), (129, 2048, 64, 8, 9), (256, 64, 64, 8, 7),
+                                       (257, 64, 72, 16, 300), (1000, 128, 264, 32, 1), (4096, 72, 40, 64, 64),
                                        (8192, 40, 8, 8, 1500), (8193, 64, 48, 16, 3), (16500, 32, 24, 128, 9000),
                                        (500, 64, 64, 16, 16383), (500, 64, 64, 16, 16384), (500, 64, 64, 16, 20000)])
 def test_many_rows_in_any_order(T, K, N, R, L):
