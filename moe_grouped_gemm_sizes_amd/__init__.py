@@ -859,9 +859,12 @@ def _ws_spec(ws, need: int, what: str):
 def _stream_for(t, stream):
     """The stream of a call on t's device, which has to be the current one unless a stream is given: launches go
     to the current device."""
-    if stream is None and t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"tensors on cuda:{t.get_device()}, the current device is cuda:{torch.cuda.current_device()}")
-    return _stream(stream)
+    if stream is not None:
+        return stream.cuda_stream
+    current = torch.cuda.current_device()
+    if t.get_device() != current:
+        raise ValueError(f"tensors on cuda:{t.get_device()}, the current device is cuda:{current}")
+    return torch._C._cuda_getCurrentRawStream(current)
 
 
 def _optional(t, name: str, shape, kind):
@@ -892,11 +895,9 @@ def rms_norm(x, weight, *, y=None, q=None, q_scale=None, residual=None, sum_out=
             raise ValueError("scale_km applies to e4m3 operands with fp32 scales")
         code, q_spec, scale_spec = BF16, _ABSENT, _ABSENT
     else:
-        _matrix(q, "q", (_E4M3,))
-        _, code, q_spec, scale_spec = _row_operand(q, "q", q_scale, K, scale_km)
-        q_spec = (q, "q", (T, K), _E4M3)
-        if q.shape[0] != T:
+        if _matrix(q, "q", (_E4M3,)) != (T, K):
             _need(q, "q", (T, K), (_E4M3,))
+        _, code, q_spec, scale_spec = _row_operand(q, "q", q_scale, K, scale_km)
     if residual is None:
         _none(sum_out, "sum_out", "without a residual")
     px, pr, pw, ps, py, pq, pqs, pd = _pointers(
