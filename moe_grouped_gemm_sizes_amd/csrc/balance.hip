@@ -5,6 +5,9 @@
 // its sigmoids over their sum), c_e the assignments of expert e and P_e the mean
 // of p_e over the tokens:
 //     loss = E / (k n) sum_e c_e P_e,    z = mean of (ln sum_e e^logit)^2.
+//
+// Logits are few bytes (8191 tokens over 256 experts: 8 MB, 1.6 us): launches and chains
+// of dependent loads bound these calls, so loads are sent as early as they can be.
 #include <hip/hip_runtime.h>
 
 #include "block.hpp"
@@ -269,7 +272,8 @@ __global__ __launch_bounds__((kTileWaves<VPL, LPT> * 64)) void balance_tile_kern
 }
 
 // A workgroup adds a sequence's rows in order: experts along the threads, and
-// every (1024 / experts)-th row a group of threads.
+// every (1024 / experts)-th row a group of threads, four rows on their way at a time.  3.5 to 5.5 us
+// (5.4 to 8.4 us with the rows one by one and 64-bit sums through LDS).
 __global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a) {
     __shared__ double p_s[1024], part_s[16];
     __shared__ int n_s[1024];
@@ -317,7 +321,8 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a) {
 // ----------------------------------------------------------------- backward
 
 // g_e = d_loss E c_e / (k n^2); softmax: p (g - <p, g>) + d_z 2 lse / n p;
-// sigmoids: p (1 - sigmoid) (g - <p, g>).
+// sigmoids: p (1 - sigmoid) (g - <p, g>).  A token a group of lanes and no loop: 8191 tokens over 160
+// experts on top of what was there, 7 us, 1.75 of them a launch.
 template <int VPL, int LPT>
 __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceBackwardArgs a) {
     constexpr int kTokens = 64 / LPT;
