@@ -781,8 +781,8 @@ typedef enum { MOEGG_WEIGHT_FP32 = 0, MOEGG_WEIGHT_BF16 = 1 } moegg_weight_t;
  *   y            bf16 [T, K] or NULL: bf16_rne(h * rstd * weight).
  *   q, q_scale   q_dtype MOEGG_FP8_E4M3, MOEGG_FP8_E4M3_SCALE_KM or
  *                MOEGG_FP8_E4M3_E8M0: e4m3 codes [T, K] of h * rstd * weight (fp32)
- *                and their scales as for moegg_dispatch's A, with a quotient within 2
- *                ulp.  MOEGG_BF16: NULL, and y is not.
+ *                and their scales as for moegg_dispatch's A.  MOEGG_BF16: NULL, and y
+ *                is not.
  *   weight       fp32 or bf16 [K].
  * The squares are summed in fp32; a row past its range is summed scaled, so that
  * every finite row has its norm.  A row with an infinity has rstd 0, NaN where the

@@ -143,7 +143,7 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a, int waves) {
         if (FMT != kBf16) {
             const GroupScale g = group_scale<FMT == kE8m0>(max16(amax8(f, 0.f)));
             uint32_t codes[2];
-            quantize<8>(f, g, codes);
+            quantize<8, FMT != kE8m0>(f, g, codes);   // bf16 values times rstd and a weight: the rounded quotient
             if (n > 0) {
                 *(u32x2*)((uint8_t*)a.q + at + c) = u32x2{codes[0], codes[1]};
                 if ((threadIdx.x & 15) == 0) {
