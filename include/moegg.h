@@ -784,9 +784,9 @@ typedef enum { MOEGG_WEIGHT_FP32 = 0, MOEGG_WEIGHT_BF16 = 1 } moegg_weight_t;
  *                and their scales as for moegg_dispatch's A.  MOEGG_BF16: NULL, and y
  *                is not.
  *   weight       fp32 or bf16 [K].
- * The squares are summed in fp32; a row past its range is summed scaled, so that
- * every finite row has its norm.  A row with an infinity has rstd 0, NaN where the
- * infinity is and 0 elsewhere; a row with a NaN is NaN.
+ * The squares are summed in fp32; a row past its range, by itself or with eps, is
+ * summed scaled, so that every finite row has its norm.  A row with an infinity has
+ * rstd 0, NaN where the infinity is and 0 elsewhere; a row with a NaN is NaN.
  * K = 1..32768 (UNSUPPORTED beyond), K % 128 == 0 with q; T up to 2097151; eps
  * from 2^-126 up, finite.  With q x, residual, sum_out, y, q and weight are 16-byte
  * aligned, else bf16 2, fp32 4; scales 4.

@@ -105,15 +105,16 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a, int waves) {
         for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(f[j], f[j], sum);
     }
     sum = part.sum(sum, part_s[0]);
-    // some row's squares past fp32's range, or an infinity or NaN in it: with rows of several waves all of the
-    // workgroup's take part in a second sum
-    bool far = !(sum < __builtin_inff());
+    // some row's squares past fp32's range, by themselves or with eps, or an infinity or NaN in it: with rows of
+    // several waves all of the workgroup's take part in a second sum
+    const float square = sum / (float)a.K + a.eps;
+    bool far = !(square < __builtin_inff());
     if (waves > 1 && (int)blockDim.x > waves * 64) {
-        float all = 0.f;
+        float all = a.eps;
         for (int w = 0; w < (int)blockDim.x / 64; ++w) all += part_s[0][w];
-        far = !(all < __builtin_inff());
+        far = !(all < 0x1p127f);                             // another order of sums than a row's: not to the last bit
     }
-    float rstd = rsqrt_f32(sum / (float)a.K + a.eps);
+    float rstd = rsqrt_f32(square);
     if (far) {
         float s = 0.f;
 #pragma unroll
@@ -127,7 +128,8 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a, int waves) {
             }
         }
         s = part.sum(s, part_s[1]);
-        if (!(sum < __builtin_inff())) rstd = rsqrt_f32(s / (float)a.K) * 0x1p-80f;
+        // an eps that is lost at this scale is nothing beside the squares
+        if (!(square < __builtin_inff())) rstd = rsqrt_f32(s / (float)a.K + a.eps * 0x1p-80f * 0x1p-80f) * 0x1p-80f;
     }
     if (width == 0) return;
     if (a.rstd && part.thread == 0) a.rstd[t] = rstd;
