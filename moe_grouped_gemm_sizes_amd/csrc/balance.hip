@@ -351,7 +351,7 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceBackwardAr
     const bool in = row >= start && row < end;
     const float n = (float)max(end - start, 1);
     const float c = in ? a.d_loss[s] * ((float)a.E / (float)a.k) / n / n : 0.f;
-    const float dz = in && a.d_z ? 2.f * a.d_z[s] / n : 0.f;
+    const float dz = in && a.d_z ? a.d_z[s] / n : 0.f;
     const float lse = probabilities<VPL, LPT>(l, a.sigmoid, p);
     float d = 0.f;
 #pragma unroll
@@ -366,7 +366,7 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceBackwardAr
         o[i] = p[i] * (o[i] - d);
         // 1 - sigmoid(x) = sigmoid(-x), without the subtraction
         if (a.sigmoid) o[i] = p[i] > 0.f ? o[i] / (1.f + expf(l[i])) : 0.f;
-        else o[i] = __builtin_fmaf(p[i], dz * lse, o[i]);
+        else o[i] = __builtin_fmaf(2.f, p[i] * dz * lse, o[i]);   // p first: 0 beside an infinite logit's lse
     }
     if (t >= a.T) return;
 #pragma unroll
