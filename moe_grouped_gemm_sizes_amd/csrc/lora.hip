@@ -238,11 +238,12 @@ __global__ __launch_bounds__(kThreads) void lora_shrink_kernel(LoraArgs a, int s
 // ----------------------------------------------------------------- U B^T
 
 // U in two bf16, the value and what is left of it (2^-16 of it is lost at most): one
-// would put half a step of bf16, 2^-8, on every term.
+// would put half a step of bf16, 2^-8, on every term.  The first is a number, so that fp32
+// past bf16's last one has its rest in the second, as have infinities and NaN.
 __device__ __forceinline__ void split_bf16(float u, uint16_t& hi, uint16_t& lo) {
-    const __bf16 h = (__bf16)u;
-    const float left = u - (float)h;
-    const __bf16 l = (__bf16)(fabsf(left) < __builtin_inff() ? left : 0.f);
+    constexpr float most = 0x1.FEp+127f;
+    const __bf16 h = (__bf16)__builtin_amdgcn_fmed3f(u, -most, most);
+    const __bf16 l = (__bf16)(u - (float)h);
     hi = __builtin_bit_cast(uint16_t, h);
     lo = __builtin_bit_cast(uint16_t, l);
 }
