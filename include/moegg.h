@@ -885,8 +885,8 @@ size_t moegg_lora_workspace_bytes(int T, int K, int R);
  * 2^-16 of it); scale and Y come in fp32, with one rounding at the end.  Only
  * adapters that some row has are read.  Two launches up to 128 rows or from 16384
  * adapters on, else three.
- * K, N and R are multiples of 8, R = 8..128, T up to 2^24 and T / 64 * N / 256 up to
- * 2^23: UNSUPPORTED otherwise.  X, A, B, Y and out 16-byte aligned, scale and adapter 4.
+ * K, N and R are multiples of 8, R = 8..128, K and N up to 2^30, T up to 2^24 and
+ * ceil(T / 64) * ceil(N / 256) up to 8380415: UNSUPPORTED otherwise.  X, A, B, Y and out 16-byte aligned, scale and adapter 4.
  * ws: moegg_lora_workspace_bytes(T, K, R), 256-byte aligned.
  */
 moegg_status_t moegg_lora(const void* X, const void* A, const void* B, const float* scale, const int32_t* adapter,
