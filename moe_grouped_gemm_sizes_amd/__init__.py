@@ -857,9 +857,13 @@ def _ws_spec(ws, need: int, what: str):
 
 
 def _stream_for(t, stream):
-    """The stream of a call on t's device, which has to be the current one unless a stream is given: launches go
-    to the current device."""
+    """The stream of a call on t's device, which has to be the current one unless a stream of it is given: launches go
+    to the stream's device, those of a default stream (handle 0) to the current one."""
     if stream is not None:
+        if stream.device_index != t.get_device():
+            raise ValueError(f"tensors on cuda:{t.get_device()}, stream of cuda:{stream.device_index}")
+        if stream.cuda_stream == 0 and torch._C._cuda_getDevice() != t.get_device():
+            raise ValueError(f"default stream of cuda:{t.get_device()}, the current device is another")
         return stream.cuda_stream
     current = torch.cuda.current_device()
     if t.get_device() != current:
