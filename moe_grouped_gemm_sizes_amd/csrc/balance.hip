@@ -167,7 +167,9 @@ struct Bounds {
 // while their sequences are looked up; a sequence's sums are in registers until it
 // ends.  8191 tokens over 256 experts in 16 sequences: 7 us, of which a launch is 1.75 and
 // three loads one after the other most of the rest (11 us with the sequences looked up first, in 4
-// waves of 8 tokens).
+// waves of 8 tokens); over 1024 experts 16 us.  Sequences of a tile come one after the other, 0.6 us
+// each with their two barriers: 32 tokens in one 4.4 us, in 16 of them 13 us; 4096 tokens over 64
+// experts in one 4.1 us, in 1000 of them 15 to 18 us.
 constexpr int kTileStep = 32;
 template <int VPL, int LPT>
 constexpr int kTileWaves = VPL == 16 || LPT == 16 ? 8 : 16;  // LDS for 1024 experts; 4 tokens a wave up to 64
@@ -272,8 +274,11 @@ __global__ __launch_bounds__((kTileWaves<VPL, LPT> * 64)) void balance_tile_kern
 }
 
 // A workgroup adds a sequence's rows in order: experts along the threads, and
-// every (1024 / experts)-th row a group of threads, four rows on their way at a time.  3.5 to 5.5 us
-// (5.4 to 8.4 us with the rows one by one and 64-bit sums through LDS).
+// every (1024 / experts)-th row a group of threads, four rows on their way at a time.  A turn of
+// these is a trip to what other XCDs wrote, and one sequence of 8191 tokens has 256 rows: 4.9 us over
+// 64 experts (4 turns), 11 us over 256 (16), 21 over 512 and 38 over 1024 (64).  In 16
+// sequences over 256 experts 4.2 to 5.7 us (8.4 us with the rows one by one and 64-bit sums through
+// LDS).
 __global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a) {
     __shared__ double p_s[1024], part_s[16];
     __shared__ int n_s[1024];
@@ -322,7 +327,7 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a) {
 
 // g_e = d_loss E c_e / (k n^2); softmax: p (g - <p, g>) + d_z 2 lse / n p;
 // sigmoids: p (1 - sigmoid) (g - <p, g>).  A token a group of lanes and no loop: 8191 tokens over 160
-// experts on top of what was there, 7 us, 1.75 of them a launch.
+// experts on top of what was there, in 1 or 5 sequences, 7 us, 1.75 of them a launch (in 1000: 8.7 us).
 template <int VPL, int LPT>
 __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceBackwardArgs a) {
     constexpr int kTokens = 64 / LPT;

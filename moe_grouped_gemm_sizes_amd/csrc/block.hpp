@@ -15,8 +15,9 @@ constexpr int kBalanceMaxExperts = 1024;
 constexpr int kBalanceMaxSequences = 65536;
 constexpr int kLoraChunk = 64;           // rows whose adapters one wave looks at together
 // Rows up to which chunks are taken as they come, and sorted beyond (us, 7168 -> 16 -> 4096; rows of 64 adapters in
-// any order: 64 rows 15.1 and 15.7 sorted, 128 20.9 and 17.2, 256 32.8 and 18.3; rank 64, 32 adapters: 18.0 and 19.0,
-// 25.2 and 19.4, 48.6 and 20.6; packed rows of 4 adapters: 11.3 and 13.7, 11.5 and 16.8, 14.1 and 18.7).
+// any order, some of them popular: 64 rows 13.5 and 13.9 sorted, 128 18.7 and 15.3, 256 31.5 and 18.4; rank 64, 32
+// adapters: 17.7 and 17.8, 23.0 and 20.8, 47.5 and 25.3; packed rows of 4 adapters: 10.7 and 14.8, 11.2 and 17.0, 13.5
+// and 17.9, which 129 to 256 rows pay for those in any order).
 constexpr int kLoraChunkRows = 128;
 constexpr int kLoraWindow = 8192;        // rows that one workgroup sorts by adapter
 constexpr int kLoraMaxSorted = 16384;    // adapters whose counts are 64 KB of LDS
@@ -120,9 +121,10 @@ inline int64_t lora_tile_slots(int T) {
 
 // Parts of K that workgroups of the first product take: 2 units of 128 columns a wave (1 where
 // rows are few), and no more of them than make 512 workgroups of full tiles, or 256 past a rank of
-// 32, whose sums are more to add (8191 rows, 2048 -> 64 -> 7168: 512 92 us, 256 86 us; 4096 rows,
-// 7168 -> 16 -> 4096: 40 and 42 us, 1024 44 us).  Rows in chunks are taken to share an adapter in
-// pairs (96 rows, 64 adapters: 18.1 us; all 64 alike 18.6 us, none 18.4 us).
+// 32, whose sums are more to add (8191 rows, 2048 -> 64 -> 7168: 512 90 us, 256 85 us; 4096 rows,
+// 7168 -> 16 -> 4096: 40 and 42 us, 1024 45 us).  Rows in chunks are taken to share an adapter in
+// pairs (96 rows of 64 adapters, ranks 16, 64 and 128: 16.5, 27.7 and 48.4 us; as if all 64 were alike
+// 17.3, 26.8 and 46.2 us, none 16.8, 26.6 and 49.1 us).
 inline int lora_splits(int T, int K, int R) {
     const int each = T <= kLoraChunkRows ? 2 : kLoraChunk, most = R <= 32 ? 512 : 256;
     const int tiles = (T + each - 1) / each, units = (K + 127) / 128;

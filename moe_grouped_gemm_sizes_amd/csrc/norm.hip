@@ -70,8 +70,9 @@ __device__ __forceinline__ float rsqrt_f32(float x) {
 
 // A row is held in registers, so that it is read once: h = bf16(x + r), the sum of h^2 in fp32,
 // then h rstd w.  4096 rows of 7168 with a residual, into bf16 and e4m3 with transposed scales: 49 us,
-// 5.4 TB/s (stores through the caches: 52 us); one row 3.3 us, a launch and a chain of load, sum and
-// store.
+// 5.4 TB/s (stores through the caches: 52 us), with E8M0 scales alike; of 12288, 16384 and 32768: 83,
+// 110 and 234 us, 5.2 to 5.5 TB/s.  One row 3.3 us, a launch and a chain of load, sum and store (of
+// 32768 columns 7.2 us).
 template <OperandFormat FMT, int CH>
 __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a, int waves) {
     __shared__ float part_s[2][16];
@@ -206,7 +207,10 @@ struct BackwardPiece {
 };
 
 // 4096 rows of 7168 with d_sum: 46 us, 5.1 TB/s, and 4.5 us for the partial rows (58 us for both
-// with each row loaded after the one before it, 57 us with one row ahead, 51 us with two).
+// with each row loaded after the one before it, 57 us with one row ahead, 51 us with two).  Rows past
+// 8192 columns are read twice, one at a time: 4096 of 12288, 16384 and 32768 take 111, 130 and 477 us
+// with the partial rows, 3.6, 4.1 and 2.3 TB/s of what has to move, the last with 83 registers spilled;
+// one row 12.5, 15 and 40 us.
 template <int CH>
 __global__ __launch_bounds__(1024) void rms_norm_backward_kernel(NormArgs a, int waves) {
     // what the workgroup's groups of waves add up to: of rows of up to 8192 columns, which may have several groups
